@@ -328,6 +328,92 @@ MOE_API moe_status moe_route_static(moe_t ctx, int T, const void* x_bf16,
                                     int32_t* topk_idx, float* topk_w, int32_t* expert_offsets,
                                     int32_t* perm, int32_t* inv_perm, moe_stream_t stream);
 
+/* ---- Training and the block around the layer ---------------------------------------------
+ * The pages fine-tune the layer's model in bf16 and serve it inside pre-norm transformer blocks
+ * (Persona Kappa forum post, "Techniques That Made It Fit"; kappa-20b-131k card, "Model
+ * Details"); they print no formula for either.  These calls are the pieces: the expert products
+ * with both their gradients, the activation between them with its gradient, and the norms around
+ * the block with theirs.  With moe_route, moe_permute and moe_combine they make a training step
+ * of the layer's expert half:
+ *   forward    gu = x_perm W_gate_up;  h = row_w silu(g) u;  y = h W_down;  out = combine(y)
+ *   backward   dy = permute(dout);  dh = dy W_down^T;  dW_down = h^T dy;
+ *              (dgu, drow_w) = swiglu backward;  dx_perm = dgu W_gate_up^T;
+ *              dW_gate_up = x_perm^T dgu;  dx = combine(dx_perm)
+ * All of them run on the current device, which must be the handle's (MOE_ERR_ARG otherwise), and
+ * only enqueue work on `stream`; none allocates, synchronises or keeps anything between calls.
+ * Every sum is fp32; results of one build on one device do not change from call to call. */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+
+/* Products grouped by expert.  The handle's E experts; W [E, K, N] bf16, K and N multiples of 8 up
+ * to 32768 (they need not be the handle's H and I).  Rows are in expert order: expert e owns rows
+ * [offsets[e], offsets[e+1]) of the R rows (offsets [E + 1] int32, device memory: moe_route's
+ * expert_offsets, or any other non-decreasing run inside 0..R).  Segments may be empty and of any
+ * length; 0 <= R <= 2^28.  Rows outside every segment are not read, and their results are left as
+ * they were.  Offsets that are negative, decrease or pass R make moe_sync_status return
+ * MOE_ERR_ARG; their segments count as empty.
+ * moe_grouped_matmul: transpose = 0:  out[r, :] = x_rows[r, :] W[e]      x [R, K], out [R, N]
+ *                     transpose = 1:  out[r, :] = x_rows[r, :] W[e]^T    x [R, N], out [R, K]
+ *   out is bf16 (one rounding, to nearest even) or fp32.  R = 0 is a no-op.
+ * moe_grouped_wgrad:  dW[e] [K, N] = sum over e's rows of x_rows[r, :]^T dy_rows[r, :], bf16 or
+ *   fp32, written whole: experts without rows get zeros (R = 0: all of it).
+ * Infinities and NaN in a row, or in an expert's weights, reach the results of that row or expert
+ * as in any matrix product, and no others. */
+MOE_API moe_status moe_grouped_matmul(moe_t ctx, int R, int K, int N, int transpose,
+                                      const int32_t* offsets, const void* x_rows_bf16,
+                                      const void* W_bf16, void* out, moe_dtype out_type,
+                                      moe_stream_t stream);
+MOE_API moe_status moe_grouped_wgrad(moe_t ctx, int R, int K, int N, const int32_t* offsets,
+                                     const void* x_rows_bf16, const void* dy_rows_bf16, void* dW,
+                                     moe_dtype out_type, moe_stream_t stream);
+
+/* SwiGLU on R rows gu [R, 2I] bf16 (gate columns [0, I), up columns [I, 2I); I the handle's):
+ *   h[r, i] = row_w[r] * silu(g[r, i]) * u[r, i]            h [R, I] bf16
+ * row_w [R] fp32, the routing weight of each row (moe_permute), or NULL for 1.
+ * Backward, with s = 1 / (1 + exp(-g)):
+ *   du = row_w dh g s;  dg = row_w dh u s (1 + g (1 - s));  drow_w[r] = sum_i dh g s u
+ * dgu [R, 2I] bf16; drow_w [R] fp32, or NULL (it needs row_w).  0 <= R <= 2^28. */
+MOE_API moe_status moe_swiglu(moe_t ctx, int R, const void* gu_bf16, const float* row_w,
+                              void* h_bf16, moe_stream_t stream);
+MOE_API moe_status moe_swiglu_backward(moe_t ctx, int R, const void* dh_bf16, const void* gu_bf16,
+                                       const float* row_w, void* dgu_bf16, float* drow_w,
+                                       moe_stream_t stream);
+
+/* The norms around a block (this layer, or any other whose output is [T, H]; H the handle's), in
+ * one pass: the norm after the block, its gate and scale, the residual, and the norm before the
+ * next block.  rms(v) = sqrt(mean(v^2) + eps), eps > 0.
+ *   n          = y / rms(y) * w_post                  (w_post NULL: n = y)
+ *   resid_out  = resid + scale * gate * n             (gate NULL: 1), rounded to resid's type
+ *   x          = resid_out / rms(resid_out) * w_next  (w_next NULL: no x)
+ * y NULL: the norm before a first block alone, x = resid / rms(resid) * w_next (then w_post, gate,
+ * resid_out and rstd_post are NULL).  resid and resid_out [T, H] are of resid_type, y [T, H] of
+ * y_type, x [T, H] bf16; w_post, gate, w_next [H] fp32; rstd_post (with w_post) and rstd_next (with
+ * w_next) [T] fp32 receive 1 / rms for the backward pass.  resid_out may be resid itself; no other
+ * buffers may overlap.  0 <= T <= 2^20.
+ *
+ * Backward: dresid [T, H] is the gradient that reaches resid_out from elsewhere (NULL: none; it
+ * may only be NULL with w_next), dx that of x; resid is the forward call's resid_out (its resid
+ * where y was NULL), y, rstd_post, rstd_next and the vectors are those of that call.  Writes
+ *   dresid_out [T, H] (resid_type; may be dresid itself)   gradient of resid
+ *   dy [T, H] (dy_type)                                    gradient of y (NULL where y was)
+ *   dw_post, dgate, dw_next [H] fp32                       where w_post, gate, w_next are given
+ * y is only read with w_post or gate and may be NULL otherwise.  workspace: at least
+ * moe_block_norm_workspace_bytes(ctx, T) bytes where any of the three vectors is given (the
+ * column sums' partial rows; calls that run at the same time need one each). */
+MOE_API moe_status moe_block_norm(moe_t ctx, int T, moe_dtype resid_type, moe_dtype y_type,
+                                  const void* resid, const void* y, const float* w_post,
+                                  const float* gate, float scale, const float* w_next, float eps,
+                                  void* resid_out, void* x_bf16, float* rstd_post,
+                                  float* rstd_next, moe_stream_t stream);
+MOE_API size_t moe_block_norm_workspace_bytes(moe_t ctx, int T);
+MOE_API moe_status moe_block_norm_backward(moe_t ctx, int T, moe_dtype resid_type,
+                                           moe_dtype y_type, moe_dtype dy_type, const void* dresid,
+                                           const void* dx_bf16, const void* resid, const void* y,
+                                           const float* rstd_post, const float* rstd_next,
+                                           const float* w_post, const float* gate, float scale,
+                                           const float* w_next, void* dresid_out, void* dy,
+                                           float* dw_post, float* dgate, float* dw_next,
+                                           void* workspace, size_t ws_bytes, moe_stream_t stream);
+
 /* Self-test of the device timeout path: launches one kernel that waits on a barrier nothing
  * completes, with a limit of `limit_us` microseconds (1..1000000), after which it sets the
  * status word and returns.  The next moe_sync_status then returns MOE_ERR_TIMEOUT.  No memory

@@ -8,6 +8,9 @@ the compiled library -- there is no CPU fallback.
     layer = Moe(E=32, H=2880, I=2880, k=4)
     out = layer.forward(x, W_router, b_router, W_gate_up, W_down)   # out [T, H] fp32
     r = layer.route(x, W_router, b_router)   # topk_idx, topk_w, expert_offsets, perm, inv_perm
+
+The pieces of a training step (grouped_matmul, grouped_wgrad, swiglu, swiglu_backward) and the
+norms around the block (block_norm, block_norm_backward, block) are methods of the same class.
 """
 from __future__ import annotations
 
@@ -30,9 +33,11 @@ MOE_OK, MOE_ERR_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_DEVICE = 4, 5, 6
 MOE_PATH_AUTO, MOE_PATH_STREAM, MOE_PATH_GEMM, MOE_PATH_TILE = 0, 1, 2, 3
 MOE_PROFILE_KINDS = 10
+MOE_BF16, MOE_F32 = 0, 1
 
 # Every entry point of include/moe.h: name -> (restype, argtypes)
 _c_int, _vp, _sz = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_c_float = ctypes.c_float
 _SIGS = {
     "moe_create": (_c_int, [_c_int, _c_int, _c_int, _c_int, ctypes.POINTER(_vp)]),
     "moe_destroy": (_c_int, [_vp]),
@@ -65,6 +70,17 @@ _SIGS = {
     "moe_combine": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp]),
     "moe_last_dispatch": (_c_int, [_vp, _c_int, _c_int, _vp, _sz, _vp, _vp]),
     "moe_route_static_max_bytes": (_sz, []),
+    "moe_grouped_matmul": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_int,
+                                    _vp]),
+    "moe_grouped_wgrad": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_int, _vp]),
+    "moe_swiglu": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp]),
+    "moe_swiglu_backward": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_block_norm": (_c_int, [_vp, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp, _c_float, _vp,
+                                _c_float, _vp, _vp, _vp, _vp, _vp]),
+    "moe_block_norm_workspace_bytes": (_sz, [_vp, _c_int]),
+    "moe_block_norm_backward": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp,
+                                         _vp, _vp, _vp, _vp, _c_float, _vp, _vp, _vp, _vp, _vp, _vp,
+                                         _vp, _sz, _vp]),
     "moe_route_static": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -105,6 +121,17 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+_DTYPES = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
+def _dtype(t, name: str) -> int:
+    """moe_dtype of a tensor or a torch.dtype."""
+    d = t.dtype if isinstance(t, torch.Tensor) else t
+    if d not in _DTYPES:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, got {d}")
+    return _DTYPES[d]
+
+
 class Moe:
     """One MoE layer shape (E experts, hidden H, intermediate I, top-k) bound to the current device."""
 
@@ -114,6 +141,7 @@ class Moe:
         _check(moe_create(E, H, I, k, ctypes.byref(h)), "moe_create")
         self._h = h
         self._ws = None
+        self._device = torch.device("cuda", torch.cuda.current_device())
 
     # -- lifetime --------------------------------------------------------------------
     def close(self):
@@ -254,6 +282,156 @@ class Moe:
                          _ptr(out, torch.float32, "out", (T, self.H)), _stream(stream))
         _check(st, "moe_combine")
         return out
+
+    # -- training and the block around the layer (include/moe.h) ------------------------
+    # Result tensors and workspaces that a call makes belong to the stream it runs on.
+    def _on(self, stream, *tensors):
+        """Context of one call: its tensors must be on the handle's device, which becomes current,
+        and what it allocates belongs to the stream it enqueues on."""
+        for t in tensors:
+            if t is not None and t.device != self._device:
+                raise ValueError(f"tensors must be on {self._device}, got one on {t.device}")
+        return torch.cuda.stream(torch.cuda.current_stream(self._device) if stream is None else stream)
+
+    def grouped_matmul(self, x_rows, W, offsets, transpose: bool = False, out=None,
+                       out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
+        """x_rows[r] @ W[e] (transpose: @ W[e].T) for the rows offsets[e] <= r < offsets[e+1] of
+        every expert e.  W [E, K, N]; offsets [E + 1] int32.  `out` (bf16 or fp32) keeps its rows
+        outside the segments; without it they are not set."""
+        if W.dim() != 3 or x_rows.dim() != 2:
+            raise ValueError("x_rows must be [R, K] (transpose: [R, N]) and W [E, K, N]")
+        E, K, N = W.shape
+        ins, outs = (N, K) if transpose else (K, N)
+        R = x_rows.shape[0]
+        with self._on(stream, x_rows, W, offsets, out):
+            if out is None:
+                out = torch.empty((R, outs), dtype=out_dtype, device=x_rows.device)
+            st = moe_grouped_matmul(
+                self._h, R, K, N, int(transpose), _ptr(offsets, torch.int32, "offsets", (self.E + 1,)),
+                _ptr(x_rows, torch.bfloat16, "x_rows", (R, ins)),
+                _ptr(W, torch.bfloat16, "W", (self.E, K, N)), _ptr(out, out.dtype, "out", (R, outs)),
+                _dtype(out, "out"), _stream(None))
+        _check(st, "moe_grouped_matmul")
+        return out
+
+    def grouped_wgrad(self, x_rows, dy_rows, offsets, out=None, out_dtype=torch.bfloat16,
+                      stream=None) -> torch.Tensor:
+        """dW [E, K, N]: dW[e] = x_rows[rows of e].T @ dy_rows[rows of e], zeros without rows."""
+        if x_rows.dim() != 2 or dy_rows.dim() != 2:
+            raise ValueError("x_rows must be [R, K] and dy_rows [R, N]")
+        (R, K), N = x_rows.shape, dy_rows.shape[1]
+        with self._on(stream, x_rows, dy_rows, offsets, out):
+            if out is None:
+                out = torch.empty((self.E, K, N), dtype=out_dtype, device=x_rows.device)
+            st = moe_grouped_wgrad(
+                self._h, R, K, N, _ptr(offsets, torch.int32, "offsets", (self.E + 1,)),
+                _ptr(x_rows, torch.bfloat16, "x_rows", (R, K)),
+                _ptr(dy_rows, torch.bfloat16, "dy_rows", (R, N)),
+                _ptr(out, out.dtype, "out", (self.E, K, N)), _dtype(out, "out"), _stream(None))
+        _check(st, "moe_grouped_wgrad")
+        return out
+
+    def swiglu(self, gu, row_w=None, out=None, stream=None) -> torch.Tensor:
+        """row_w[r] * silu(gu[r, :I]) * gu[r, I:] -> [R, I] bf16 (row_w None: 1)."""
+        R = gu.shape[0]
+        with self._on(stream, gu, row_w, out):
+            if out is None:
+                out = torch.empty((R, self.I), dtype=torch.bfloat16, device=gu.device)
+            st = moe_swiglu(self._h, R, _ptr(gu, torch.bfloat16, "gu", (R, 2 * self.I)),
+                            _ptr(row_w, torch.float32, "row_w", (R,)),
+                            _ptr(out, torch.bfloat16, "out", (R, self.I)), _stream(None))
+        _check(st, "moe_swiglu")
+        return out
+
+    def swiglu_backward(self, dh, gu, row_w=None, stream=None) -> tuple:
+        """(dgu [R, 2I] bf16, drow_w [R] fp32, or None without row_w) from dh [R, I]."""
+        R = gu.shape[0]
+        with self._on(stream, dh, gu, row_w):
+            dgu = torch.empty((R, 2 * self.I), dtype=torch.bfloat16, device=gu.device)
+            dw = None if row_w is None else torch.empty((R,), dtype=torch.float32, device=gu.device)
+            st = moe_swiglu_backward(self._h, R, _ptr(dh, torch.bfloat16, "dh", (R, self.I)),
+                                     _ptr(gu, torch.bfloat16, "gu", (R, 2 * self.I)),
+                                     _ptr(row_w, torch.float32, "row_w", (R,)), dgu.data_ptr(),
+                                     _ptr(dw, torch.float32, "drow_w"), _stream(None))
+        _check(st, "moe_swiglu_backward")
+        return dgu, dw
+
+    def block_norm(self, resid, y=None, w_post=None, gate=None, scale: float = 1.0, w_next=None,
+                   eps: float = 1e-5, resid_out=None, stream=None) -> dict:
+        """The norm after a block, its gate and scale, the residual and the norm before the next
+        block in one pass.  Returns resid (the new residual: resid + scale * gate * norm(y), in
+        resid's type; resid itself without y), x (its norm, bf16; None without w_next) and
+        rstd_post, rstd_next for the backward pass."""
+        T, H = resid.shape[0], self.H
+        dev = resid.device
+        with self._on(stream, resid, y, w_post, gate, w_next, resid_out):
+            if resid_out is None and y is not None:
+                resid_out = torch.empty_like(resid)
+            x = rp = rn = None
+            if w_post is not None:
+                rp = torch.empty((T,), dtype=torch.float32, device=dev)
+            if w_next is not None:
+                x = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+                rn = torch.empty((T,), dtype=torch.float32, device=dev)
+            st = moe_block_norm(
+                self._h, T, _dtype(resid, "resid"), MOE_F32 if y is None else _dtype(y, "y"),
+                _ptr(resid, resid.dtype, "resid", (T, H)),
+                _ptr(y, None if y is None else y.dtype, "y", (T, H)),
+                _ptr(w_post, torch.float32, "w_post", (H,)), _ptr(gate, torch.float32, "gate", (H,)),
+                scale, _ptr(w_next, torch.float32, "w_next", (H,)), eps,
+                _ptr(resid_out, resid.dtype, "resid_out", (T, H)), _ptr(x, torch.bfloat16, "x"),
+                _ptr(rp, torch.float32, "rstd_post"), _ptr(rn, torch.float32, "rstd_next"),
+                _stream(None))
+        _check(st, "moe_block_norm")
+        return dict(resid=resid if y is None else resid_out, x=x, rstd_post=rp, rstd_next=rn)
+
+    def block_norm_workspace_bytes(self, T: int) -> int:
+        return moe_block_norm_workspace_bytes(self._h, T)
+
+    def block_norm_backward(self, dresid, dx, resid, y=None, rstd_post=None, rstd_next=None,
+                            w_post=None, gate=None, scale: float = 1.0, w_next=None,
+                            block: bool | None = None, dy_dtype=torch.bfloat16, stream=None,
+                            workspace=None) -> dict:
+        """Gradients of block_norm: dresid and dx are those of its two results (either may be None
+        where nothing flows), resid, rstd_post and rstd_next its results.  Returns dresid (the
+        gradient of the old residual), dy (None for the norm before a first block: `block` False,
+        the default without y), dw_post, dgate and dw_next (None where the vector is)."""
+        like = dresid if dresid is not None else resid
+        (T, H), dev = like.shape, like.device
+        has_block = (y is not None) if block is None else block
+        with self._on(stream, dresid, dx, resid, y, rstd_post, rstd_next, w_post, gate, w_next, workspace):
+            vec = lambda v: None if v is None else torch.empty((H,), dtype=torch.float32, device=dev)  # noqa: E731
+            out = dict(dresid=torch.empty((T, H), dtype=like.dtype, device=dev),
+                       dy=torch.empty((T, H), dtype=dy_dtype, device=dev) if has_block else None,
+                       dw_post=vec(w_post), dgate=vec(gate), dw_next=vec(w_next))
+            ws = workspace
+            if ws is None and not (w_post is None and gate is None and w_next is None):
+                ws = torch.empty((self.block_norm_workspace_bytes(T),), dtype=torch.uint8, device=dev)
+            f32 = torch.float32
+            st = moe_block_norm_backward(
+                self._h, T, _dtype(like, "dresid"), MOE_F32 if y is None else _dtype(y, "y"),
+                _dtype(dy_dtype, "dy_dtype"), _ptr(dresid, like.dtype, "dresid", (T, H)),
+                _ptr(dx, torch.bfloat16, "dx", (T, H)), _ptr(resid, like.dtype, "resid", (T, H)),
+                _ptr(y, None if y is None else y.dtype, "y", (T, H)),
+                _ptr(rstd_post, f32, "rstd_post", (T,)), _ptr(rstd_next, f32, "rstd_next", (T,)),
+                _ptr(w_post, f32, "w_post", (H,)), _ptr(gate, f32, "gate", (H,)), scale,
+                _ptr(w_next, f32, "w_next", (H,)), out["dresid"].data_ptr(),
+                _ptr(out["dy"], dy_dtype, "dy"), _ptr(out["dw_post"], f32, "dw_post"),
+                _ptr(out["dgate"], f32, "dgate"), _ptr(out["dw_next"], f32, "dw_next"),
+                0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _stream(None))
+        _check(st, "moe_block_norm_backward")
+        return out
+
+    def block(self, resid, x, W_router, b_router, W_gate_up, W_down, w_post=None, gate=None,
+              scale: float = 1.0, w_next=None, eps: float = 1e-5, resid_out=None, stream=None,
+              workspace=None) -> dict:
+        """The layer inside its transformer block: x is the normed residual (block_norm of the
+        previous block, or block_norm(resid, w_next=...) before the first), the layer's output goes
+        through block_norm into the residual.  Returns block_norm's dict."""
+        with self._on(stream, resid, x):
+            y = self.forward(x, W_router, b_router, W_gate_up, W_down, workspace=workspace)
+            return self.block_norm(resid, y, w_post=w_post, gate=gate, scale=scale, w_next=w_next,
+                                   eps=eps, resid_out=resid_out)
 
     def workspace_bytes_mxfp4(self, T: int) -> int:
         return moe_workspace_bytes_mxfp4(self._h, T)

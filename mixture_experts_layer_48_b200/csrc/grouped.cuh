@@ -1,0 +1,1018 @@
+// Matrix products grouped by expert, ragged sizes, forward and backward.
+//
+// R rows lie in expert order: expert e owns rows [offsets[e], offsets[e+1]) (what moe_route and
+// moe_permute produce).  W is [E, K, N], bf16; all sums are fp32 in tensor memory.
+//
+//   product            y[r, :] = x[r, :] W[e]          x [R, K] -> y [R, N]       (forward)
+//   transposed         y[r, :] = x[r, :] W[e]^T        x [R, N] -> y [R, K]       (gradient of x)
+//   weight gradient    dW[e]   = sum_r x[r, :]^T dy[r, :]   over e's rows         [E, K, N]
+//
+// Three kernel shapes, all persistent and warp-specialised (TMA producer warp, MMA issuer warp,
+// four epilogue warps) around a ring of 128-byte-swizzled shared-memory stages of 64 reduction
+// elements:
+//
+//   grouped_cols_kernel   few rows per expert, bound by reading each touched expert's weights
+//                         once from HBM: 128 weight columns are the M operand, the rows N, and a
+//                         cluster of S CTAs can split the reduction of one tile (their partial
+//                         sums meet over distributed shared memory, added in rank order, so
+//                         results do not depend on timing)
+//   grouped_rows_kernel   many rows per expert, bound by the tensor cores: 256 rows x 256 columns
+//                         per CTA pair (tcgen05 cta_group::2)
+//   grouped_wgrad_kernel  256 x 256 tiles of dW[e] per CTA pair, the expert's rows are the
+//                         reduction; both operands are MN-major
+//
+// The segments are read on the device: every CTA checks the E + 1 offsets and scans them in
+// shared memory, so there is no work-list kernel, no workspace and no host sync.  Offsets that
+// are negative, decrease or pass R give empty segments and set the status word.  Rows outside
+// every segment are neither used nor written.
+//
+// Sums: the tensor cores add into fp32 accumulators with truncation, an error that grows by about
+// 1.1e-9 (relative to the result) per reduction element (measured: 3.0e-6 at 2880, 6.3e-6 at
+// 5760, 1.9e-5 at 16384).  fp32 results therefore add reductions longer than 6144 elements up
+// from pieces of 6144 in the epilogue (round to nearest); bf16 results, whose rounding is 4e-3,
+// take one piece.
+#pragma once
+
+#include "common.cuh"
+#include "ep.cuh"
+#include "expert_gemm_mx.cuh"
+#include "gemm.cuh"
+
+namespace moe {
+
+constexpr int kGrMaxE = 256;
+constexpr int kGrBK = 64;           // reduction elements per stage (one 128-byte swizzle row)
+constexpr int kGrPieceStages = 96;  // stages per accumulator of an fp32 result (6144 elements)
+
+MOE_DEVINL void tma_load_3d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
+                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+      : "memory");
+}
+MOE_DEVINL void tma_load_3d_pair(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
+                                 uint32_t bar_cluster_addr) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(bar_cluster_addr)
+      : "memory");
+}
+// Wait that also orders the reads after writes of the other CTAs of the cluster.
+MOE_DEVINL bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+MOE_DEVINL bool wait_or_abort_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                      uint32_t* status) {
+  if (mbar_try_wait_cluster(bar, parity)) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (*abort_flag) return false;
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicOr(status, kStatusTimeout);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
+// The same answer for every lane, so that a warp leaves its loop as one (the tensor-memory loads
+// and barriers that follow are collective).
+MOE_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                          uint32_t* status) {
+  return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status));
+}
+MOE_DEVINL bool warp_wait_cluster(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                  uint32_t* status) {
+  return __all_sync(0xffffffffu, wait_or_abort_cluster(bar, parity, abort_flag, status));
+}
+// Named barrier over nthreads threads that also answers whether `ok` held for all of them.
+MOE_DEVINL bool named_bar_and(int id, int nthreads, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(nthreads), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+MOE_DEVINL float4 ld_cluster_f4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+// Expert segments in shared memory: expert e owns rows [beg[e], beg[e] + cnt[e]); its row chunks
+// are number base[e] .. base[e + 1] - 1 of the call's.
+struct Segments {
+  int32_t beg[kGrMaxE];
+  int32_t cnt[kGrMaxE];
+  int32_t base[kGrMaxE + 1];
+};
+
+// Every thread of the block; the caller synchronises the block afterwards.  Only warp 0 writes
+// base, after a barrier inside.
+MOE_DEVINL void load_segments(Segments& s, const int32_t* __restrict__ offsets, int E, int R,
+                              int chunk, uint32_t* status) {
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    const int b = offsets[e], n = offsets[e + 1];
+    const bool ok = b >= 0 && n >= b && n <= R;
+    if (!ok) atomicOr(status, kStatusBadCounts);
+    s.beg[e] = ok ? b : 0;
+    s.cnt[e] = ok ? n - b : 0;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int run = 0;
+    for (int e0 = 0; e0 < E; e0 += 32) {
+      const int e = e0 + lane;
+      const int c = e < E ? (s.cnt[e] + chunk - 1) / chunk : 0;
+      int inc = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, inc, d);
+        if (lane >= d) inc += o;
+      }
+      if (e < E) s.base[e] = run + inc - c;
+      run += __shfl_sync(0xffffffffu, inc, 31);
+    }
+    if (lane == 0) s.base[E] = run;
+  }
+}
+
+// The expert that owns tile t when an expert with c chunks has c * per tiles: the last e with
+// base[e] * per <= t.  t < base[E] * per.
+MOE_DEVINL int find_expert(const Segments& s, int E, int per, int t) {
+  const int c = t / per;
+  int lo = 0, hi = E;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.base[mid] <= c) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+struct GroupedArgs {
+  const int32_t* offsets;  // [E + 1]
+  int E, R;
+  int Kred;                // reduction length (row length of x; rows of a segment for dW)
+  int Ncols;               // columns of the result
+  int M;                   // rows of one dW[e] (weight gradient only)
+  void* out;               // [R, Ncols], or [E, M, Ncols] for the weight gradient
+  uint32_t* status;
+};
+
+// Writes 4 fp32 values as OUT (float or bf16) to 4 consecutive columns.
+template <bool F32>
+MOE_DEVINL void store4(void* out, size_t idx, float4 v, bool add) {
+  if constexpr (F32) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + idx);
+    if (add) {
+      const float4 o = *p;
+      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+    }
+    *p = v;
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + idx) =
+        make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Few rows per expert: weight columns as the M operand, rows as N.
+//
+// ROWS: rows per tile (largest MMA N).  NM: 128-column MMAs per tile.
+//   <32, 1>, <128, 1>  clusters of S CTAs split a tile's reduction
+//   <128, 2>           one CTA per tile of 256 columns: the rows are loaded once for both MMAs
+// ------------------------------------------------------------------------------------------------
+template <int ROWS, int NM>
+struct ColsCfg {
+  static constexpr bool kSplit = NM == 1;
+  static constexpr int kABytes = NM * 128 * kGrBK * 2;
+  static constexpr int kBBytes = ROWS * kGrBK * 2;
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = ROWS == 32 ? 9 : 4;
+  static constexpr int kAccBufs = 2;
+  static constexpr int kTmemCols = kAccBufs * NM * ROWS;    // 64, 256, 512: powers of two
+  static constexpr int kPitch = kSplit ? 132 : 33;          // floats per staged row
+  static constexpr int kEpiBytes = kSplit ? ROWS * kPitch * 4 : 4 * 32 * kPitch * 4;
+  static constexpr int kSmem = 1024 + kStages * kStageBytes + 256 + kEpiBytes;
+  static_assert(kStageBytes % 1024 == 0, "128-byte swizzle atoms");
+  static_assert(kSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
+};
+constexpr int kColsThreads = 192;
+constexpr int kColsRowBox = 16;   // rows per TMA box
+
+template <int ROWS, int NM, bool TRANS, bool F32>
+__global__ void __launch_bounds__(kColsThreads, 1)
+    grouped_cols_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap wmap,
+                        const __grid_constant__ CUtensorMap xmap, const int S) {
+  using C = ColsCfg<ROWS, NM>;
+  constexpr int kStages = C::kStages, kBufs = C::kAccBufs;
+  constexpr int TW = 128 * NM;                       // output columns per tile
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ Segments seg;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t* ring = align1k(smem_raw);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(ring + kStages * C::kStageBytes);
+  uint64_t* full = bars;
+  uint64_t* empty = full + kStages;
+  uint64_t* acc_full = empty + kStages;
+  uint64_t* acc_empty = acc_full + kBufs;
+  uint64_t* drain = acc_empty + kBufs;
+  uint64_t* part_full = drain + 1;    // every CTA of the cluster has its partial sums in place
+  uint64_t* part_empty = part_full + 1;  // every CTA of the cluster has read this CTA's sums
+  float* epi = reinterpret_cast<float*>(ring + kStages * C::kStageBytes + 256);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = C::kSplit ? (int)cluster_ctarank() : 0;
+
+  if (warp == 1) {
+    tmem_alloc(&s_tmem, C::kTmemCols);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < kBufs; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 128);
+    }
+    mbar_init(drain, 1);
+    mbar_init(part_full, S);
+    mbar_init(part_empty, S);
+    s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&wmap);
+    tma_prefetch_desc(&xmap);
+  }
+  pdl_wait();  // offsets, rows and weights may come from the previous kernels
+  pdl_launch_next();
+  load_segments(seg, a.offsets, a.E, a.R, ROWS, a.status);
+  tc_fence_before();
+  __syncthreads();
+  if (C::kSplit) cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem;
+
+  const int NT = (a.Ncols + TW - 1) / TW;
+  const int tiles = seg.base[a.E] * NT;
+  const int nk_all = (a.Kred + kGrBK - 1) / kGrBK;
+  const int piece = !C::kSplit && F32 ? kGrPieceStages : nk_all;
+  const int group = C::kSplit ? (int)blockIdx.x / S : (int)blockIdx.x;
+  const int groups = C::kSplit ? (int)gridDim.x / S : (int)gridDim.x;
+  volatile int* abort_flag = &s_abort;
+
+  // Tile t: the chunks of one expert and column block are neighbours, so an expert with more
+  // than one chunk re-reads its weight block from L2.
+  struct Tile { int e, row0, rows, n0; };
+  auto tile_at = [&](int t) {
+    Tile w;
+    w.e = find_expert(seg, a.E, NT, t);
+    const int chunks = seg.base[w.e + 1] - seg.base[w.e];
+    const int local = t - seg.base[w.e] * NT;
+    const int ch = local % chunks;
+    w.n0 = local / chunks * TW;
+    w.row0 = seg.beg[w.e] + ch * ROWS;
+    w.rows = min(ROWS, seg.cnt[w.e] - ch * ROWS);
+    return w;
+  };
+  // This CTA's stages of tile t: an even split over the cluster, the remainder rotated from tile
+  // to tile so that every rank streams the same bytes in the long run.
+  auto k_range = [&](int t, int& k0, int& k1) {
+    if (!C::kSplit) {
+      k0 = 0;
+      k1 = nk_all;
+      return;
+    }
+    const int q = nk_all / S, rem = nk_all - q * S;
+    const int p = (rank + t / groups) % S;
+    k0 = p * q + min(p, rem);
+    k1 = k0 + q + (p < rem ? 1 : 0);
+  };
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer ------------------------------
+    if (lane == 0) {
+      uint32_t it = 0;
+      int last_it[kStages];
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) last_it[s] = -1;
+      for (int t = group; t < tiles && !*abort_flag; t += groups) {
+        const Tile w = tile_at(t);
+        int k0, k1;
+        k_range(t, k0, k1);
+        const int nrb = (w.rows + kColsRowBox - 1) / kColsRowBox;
+        const uint32_t bytes = C::kABytes + (uint32_t)nrb * kColsRowBox * kGrBK * 2;
+        bool ok = true;
+        for (int kst = k0; kst < k1; ++kst, ++it) {
+          const int slot = it % kStages;
+          const uint32_t ph = (it / kStages) & 1u;
+          if (!wait_or_abort(&empty[slot], ph ^ 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(&full[slot], bytes);
+          uint8_t* st = ring + slot * C::kStageBytes;
+          const int k = kst * kGrBK;
+          // weight boxes past the matrix's edges are zero-filled (each expert is a plane of the
+          // map, so an edge never reads the next expert)
+          if (TRANS) {  // [columns of y, reduction]: 128 x 64 boxes, K-major
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+              tma_load_3d(st + m * 128 * kGrBK * 2, &wmap, k, w.n0 + 128 * m, w.e, &full[slot]);
+          } else {      // [reduction, columns of y]: 64 x 64 boxes, MN-major
+#pragma unroll
+            for (int b = 0; b < 2 * NM; ++b)
+              tma_load_3d(st + b * 64 * kGrBK * 2, &wmap, w.n0 + 64 * b, k, w.e, &full[slot]);
+          }
+          for (int r = 0; r < nrb; ++r)
+            tma_load_2d(st + C::kABytes + r * (kColsRowBox * kGrBK * 2), &xmap, k,
+                        w.row0 + r * kColsRowBox, &full[slot]);
+          last_it[slot] = it;
+        }
+        if (!ok) break;
+      }
+      // never leave the CTA with copies in flight
+      for (int s = 0; s < kStages; ++s)
+        if (last_it[s] >= 0 &&
+            !mbar_wait_bounded(&full[s], (last_it[s] / kStages) & 1u, kWaitLimitNs))
+          atomicOr(a.status, kStatusTimeout);
+    }
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer ------------------------------
+    if (lane == 0) {
+      const uint32_t ring_s = smem_u32(ring);
+      // descriptors of slot 0; a slot / K-step offset only moves the 14-bit start address
+      const uint64_t adesc0 = TRANS ? smem_desc_sw128(ring_s, 16, 1024)
+                                    : smem_desc_sw128(ring_s, 64 * kGrBK * 2, 1024);
+      const uint64_t bdesc0 = smem_desc_sw128(ring_s + C::kABytes, 16, 1024);
+      constexpr int kAStep = TRANS ? 32 : 16 * 128;    // bytes per 16 reduction elements
+      uint32_t it = 0;
+      int unit = 0;
+      bool issued = false, ok = true;
+      for (int t = group; ok && t < tiles && !*abort_flag; t += groups) {
+        const Tile w = tile_at(t);
+        int k0, k1;
+        k_range(t, k0, k1);
+        const int N = (w.rows + kColsRowBox - 1) / kColsRowBox * kColsRowBox;
+        const uint32_t idesc = idesc_bf16_f32(128, N, !TRANS, false);
+        for (int p0 = k0; ok && p0 < k1; p0 += piece, ++unit) {
+          const int p1 = min(k1, p0 + piece);
+          const int buf = unit % kBufs;
+          const uint32_t aph = (unit / kBufs) & 1u;
+          if (!wait_or_abort(&acc_empty[buf], aph ^ 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + buf * NM * ROWS;
+          for (int kst = p0; kst < p1; ++kst, ++it) {
+            const int slot = it % kStages;
+            const uint32_t ph = (it / kStages) & 1u;
+            if (!wait_or_abort(&full[slot], ph, abort_flag, a.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t soff = (uint64_t)((slot * C::kStageBytes) >> 4);
+#pragma unroll
+            for (int k16 = 0; k16 < kGrBK / 16; ++k16) {
+              const uint64_t ak = adesc0 + soff + ((k16 * kAStep) >> 4);
+              const uint64_t bk = bdesc0 + soff + ((k16 * 32) >> 4);
+              const uint32_t acc = kst != p0 || k16 != 0;
+#pragma unroll
+              for (int m = 0; m < NM; ++m)
+                tc_mma_bf16(d + m * ROWS, ak + ((m * 128 * kGrBK * 2) >> 4), bk, idesc, acc);
+            }
+            tc_commit(&empty[slot]);
+            issued = true;
+          }
+          if (ok) tc_commit(&acc_full[buf]);
+        }
+      }
+      if (issued) {  // all MMAs complete before the tensor memory is freed
+        tc_commit(drain);
+        if (!mbar_wait_bounded(drain, 0, kWaitLimitNs)) atomicOr(a.status, kStatusTimeout);
+      }
+    }
+  } else {
+    // ------------------------------ epilogue ------------------------------
+    // One TMEM lane (one weight column) per thread; the tile's rows are TMEM columns.
+    const int q = warp & 3;
+    int unit = 0, ti = 0;
+    bool ok = true;
+    for (int t = group; ok && t < tiles; t += groups, ++ti) {
+      const Tile w = tile_at(t);
+      int k0, k1;
+      k_range(t, k0, k1);
+      if constexpr (C::kSplit) {
+        // the previous tile's partial sums have been read by the whole cluster
+        ok = warp_wait_cluster(part_empty, (ti & 1) ^ 1u, abort_flag, a.status);
+        const int buf = unit % kBufs;
+        const bool any = k1 > k0;
+        if (ok && any) ok = warp_wait(&acc_full[buf], (unit / kBufs) & 1u, abort_flag, a.status);
+        if (ok) {
+          tc_fence_after();
+          for (int r0 = 0; r0 < w.rows; r0 += 32) {
+            float v[32];
+            if (any) {
+              tmem_ld32(tmem_base + ((uint32_t)(32 * q) << 16) + buf * ROWS + r0, v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) epi[(r0 + i) * C::kPitch + 32 * q + lane] = v[i];
+          }
+          if (any) {
+            tc_fence_before();
+            mbar_arrive(&acc_empty[buf]);
+            ++unit;
+          }
+        }
+        ok = named_bar_and(1, 128, ok);
+        if (!ok) break;
+        const int et = tid - 64;  // 0..127
+        if (et < S) mbar_arrive_cluster(mapa_shared(smem_u32(part_full), et));
+        ok = warp_wait_cluster(part_full, ti & 1, abort_flag, a.status);
+        // this rank adds and writes its share of the 128 columns, 4 per thread
+        const int quads = 32 / S;
+        for (int i = et; ok && i < w.rows * quads; i += 128) {
+          const int r = i / quads, col = 4 * (rank * quads + i % quads);
+          if (w.n0 + col >= a.Ncols) continue;
+          const uint32_t off = smem_u32(epi + r * C::kPitch + col);
+          float4 v = ld_cluster_f4(mapa_shared(off, 0));
+          for (int s = 1; s < S; ++s) {
+            const float4 o = ld_cluster_f4(mapa_shared(off, s));
+            v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+          }
+          store4<F32>(a.out, (size_t)(w.row0 + r) * a.Ncols + w.n0 + col, v, false);
+        }
+        ok = named_bar_and(1, 128, ok);
+        if (ok && et < S) mbar_arrive_cluster(mapa_shared(smem_u32(part_empty), et));
+      } else {
+        float* stage = epi + (warp - 2) * 32 * C::kPitch;
+        for (int p0 = k0; p0 < k1; p0 += piece, ++unit) {
+          const int buf = unit % kBufs;
+          if (!warp_wait(&acc_full[buf], (unit / kBufs) & 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t tb = tmem_base + ((uint32_t)(32 * q) << 16) + buf * NM * ROWS;
+#pragma unroll 1
+          for (int m = 0; m < NM; ++m) {
+            const int col0 = w.n0 + 128 * m + 32 * q;
+            if (col0 >= a.Ncols) continue;  // warp-uniform
+            for (int r0 = 0; r0 < w.rows; r0 += 32) {
+              float v[32];
+              tmem_ld32(tb + m * ROWS + r0, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) stage[i * C::kPitch + lane] = v[i];
+              __syncwarp();
+              // 8 lanes cover the 32 columns of a row
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int r = 4 * i + (lane >> 3), cc = 4 * (lane & 7);
+                const float* sp = stage + r * C::kPitch + cc;
+                if (r0 + r < w.rows && col0 + cc < a.Ncols)
+                  store4<F32>(a.out, (size_t)(w.row0 + r0 + r) * a.Ncols + col0 + cc,
+                              make_float4(sp[0], sp[1], sp[2], sp[3]), p0 > k0);
+              }
+              __syncwarp();
+            }
+          }
+          tc_fence_before();
+          mbar_arrive(&acc_empty[buf]);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (C::kSplit) cluster_sync_all();  // no CTA leaves while another reads its sums
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem_base, C::kTmemCols);
+}
+
+// ------------------------------------------------------------------------------------------------
+// CTA pairs: 256 x 256 result tiles.  Shared by the many-row product and the weight gradient.
+// ------------------------------------------------------------------------------------------------
+constexpr int kPairStages = 6;
+constexpr int kPairHalf = 128;                                 // rows and columns staged per CTA
+constexpr int kPairABytes = kPairHalf * kGrBK * 2;             // 16 KB
+constexpr int kPairStageBytes = 2 * kPairABytes;               // 32 KB per CTA
+constexpr int kPairEpiPitch = 36;                              // 32-bit words per staged row
+constexpr int kPairEpiBytes = 4 * 32 * kPairEpiPitch * 4;
+constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 256 + kPairEpiBytes;
+constexpr int kPairThreads = 192;
+constexpr int kWgradThreads = 224;                             // + the warp that masks ragged ends
+static_assert(kPairSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
+
+// One warp's 32 rows x 256 accumulator columns to `out` (row stride ld, this warp's first row and
+// the tile's first column already in row0 / n0), through a shared-memory transpose so that eight
+// lanes write 128 contiguous bytes of one row.  rows_ok: valid rows of the 32 (may be <= 0).
+// zero: write zeros instead of the accumulators.  add: fp32 results add to what is there.
+template <bool F32>
+MOE_DEVINL void pair_store(uint32_t taddr, uint32_t* stage, int lane, void* out, size_t row0,
+                           int rows_ok, int n0, int ld, bool zero, bool add) {
+  constexpr int kCols = F32 ? 32 : 64;   // columns per 128 bytes
+#pragma unroll 1
+  for (int c = 0; c < 256; c += kCols) {
+    if (n0 + c >= ld) break;             // warp-uniform
+    uint32_t w[32];
+    if (zero) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = 0u;
+    } else if constexpr (F32) {
+      float v[32];
+      tmem_ld32(taddr + c, v);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
+    } else {
+      float v[32];
+      tmem_ld32(taddr + c, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+      tmem_ld32(taddr + c + 32, v);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[16 + i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+    }
+    uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPairEpiPitch);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      mine[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    __syncwarp();
+    const int cc = n0 + c + (lane & 7) * (kCols / 8);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kPairEpiPitch + 4 * (lane & 7));
+      if (r < rows_ok && cc < ld) {
+        if constexpr (F32) {
+          float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + (row0 + r) * ld + cc);
+          float4 f = make_float4(__uint_as_float(v.x), __uint_as_float(v.y),
+                                 __uint_as_float(v.z), __uint_as_float(v.w));
+          if (add) {
+            const float4 o = *p;
+            f = make_float4(f.x + o.x, f.y + o.y, f.z + o.z, f.w + o.w);
+          }
+          *p = f;
+        } else {
+          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (row0 + r) * ld + cc) = v;
+        }
+      }
+    }
+    __syncwarp();
+  }
+}
+
+// Many rows per expert.  Tile: 256 rows of one expert x 256 columns; each CTA of the pair stages
+// its 128 rows of x (K-major) and 128 of the weight columns (MN-major, or K-major for the
+// transposed product), the even CTA issues MMAs over both, and each CTA's tensor memory receives
+// its 128 rows x 256 columns.  Rows of a chunk past the segment's end are computed (they are
+// other experts' rows, or zero past R) and never stored.
+template <bool TRANS, bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    grouped_rows_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap wmap,
+                        const __grid_constant__ CUtensorMap xmap) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ Segments seg;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t* ring = align1k(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kPairStages * kPairStageBytes);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* acc_full = empty + kPairStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* epi = reinterpret_cast<uint32_t*>(ring + kPairStages * kPairStageBytes + 256);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (warp == 1) {
+    tmem_alloc_2sm(&s_tmem, 512);
+    tmem_relinquish_2sm();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * 128);
+    }
+    mbar_init(drain, 1);
+    s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&wmap);
+    tma_prefetch_desc(&xmap);
+  }
+  pdl_wait();  // offsets, rows and weights may come from the previous kernels
+  pdl_launch_next();
+  load_segments(seg, a.offsets, a.E, a.R, 256, a.status);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem;
+
+  const int NT = (a.Ncols + 255) / 256;
+  const int tiles = seg.base[a.E] * NT;
+  const int nk = (a.Kred + kGrBK - 1) / kGrBK;
+  const int piece = F32 ? kGrPieceStages : nk;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  volatile int* abort_flag = &s_abort;
+
+  // Tile t: the column blocks of one chunk are neighbours, so the pairs that run together share
+  // a few chunks of rows and one expert's weights in L2.
+  struct Tile { int e, row0, rows, n0; };
+  auto tile_at = [&](int t) {
+    Tile w;
+    w.e = find_expert(seg, a.E, NT, t);
+    const int local = t - seg.base[w.e] * NT;
+    const int ch = local / NT;
+    w.n0 = (local - ch * NT) * 256;
+    w.row0 = seg.beg[w.e] + ch * 256;
+    w.rows = min(256, seg.cnt[w.e] - ch * 256);
+    return w;
+  };
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer (both CTAs) ------------------------------
+    if (lane == 0) {
+      uint32_t it = 0;
+      int last_it[kPairStages];
+#pragma unroll
+      for (int s = 0; s < kPairStages; ++s) last_it[s] = -1;
+      for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+        const Tile w = tile_at(t);
+        const int row0 = w.row0 + rank * kPairHalf, col0 = w.n0 + rank * kPairHalf;
+        bool ok = true;
+        for (int kst = 0; kst < nk; ++kst, ++it) {
+          const int slot = it % kPairStages;
+          const uint32_t ph = (it / kPairStages) & 1u;
+          if (!wait_or_abort(&empty[slot], ph ^ 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t bar = mapa_shared(smem_u32(&full[slot]), 0);
+          if (leader) mbar_arrive_expect_tx(&full[slot], 2 * kPairStageBytes);
+          uint8_t* st = ring + slot * kPairStageBytes;
+          const int k = kst * kGrBK;
+          tma_load_2d_pair(st, &xmap, k, row0, bar);
+          if (TRANS) {
+            tma_load_3d_pair(st + kPairABytes, &wmap, k, col0, w.e, bar);
+          } else {
+            tma_load_3d_pair(st + kPairABytes, &wmap, col0, k, w.e, bar);
+            tma_load_3d_pair(st + kPairABytes + 64 * kGrBK * 2, &wmap, col0 + 64, k, w.e, bar);
+          }
+          last_it[slot] = it;
+        }
+        if (!ok) break;
+      }
+      // the even CTA's full barriers count both CTAs' copies: drain them before the pair exits
+      if (leader)
+        for (int s = 0; s < kPairStages; ++s)
+          if (last_it[s] >= 0 &&
+              !mbar_wait_bounded(&full[s], (last_it[s] / kPairStages) & 1u, kWaitLimitNs))
+            atomicOr(a.status, kStatusTimeout);
+    }
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer (even CTA) ------------------------------
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, false, !TRANS);
+      const uint32_t ring_s = smem_u32(ring);
+      const uint64_t adesc0 = smem_desc_sw128(ring_s, 16, 1024);
+      const uint64_t bdesc0 = TRANS ? smem_desc_sw128(ring_s + kPairABytes, 16, 1024)
+                                    : smem_desc_sw128(ring_s + kPairABytes, 64 * kGrBK * 2, 1024);
+      constexpr int kBStep = TRANS ? 32 : 16 * 128;
+      uint32_t it = 0;
+      int unit = 0;
+      bool issued = false, ok = true;
+      for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
+        for (int p0 = 0; ok && p0 < nk; p0 += piece, ++unit) {
+          const int p1 = min(nk, p0 + piece);
+          const int buf = unit & 1;
+          if (!wait_or_abort(&acc_empty[buf], ((unit >> 1) & 1u) ^ 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + buf * 256;
+          for (int kst = p0; kst < p1; ++kst, ++it) {
+            const int slot = it % kPairStages;
+            if (!wait_or_abort(&full[slot], (it / kPairStages) & 1u, abort_flag, a.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t soff = (uint64_t)((slot * kPairStageBytes) >> 4);
+#pragma unroll
+            for (int k16 = 0; k16 < kGrBK / 16; ++k16)
+              tc_mma_bf16_2sm(d, adesc0 + soff + ((k16 * 32) >> 4),
+                              bdesc0 + soff + ((k16 * kBStep) >> 4), idesc,
+                              kst != p0 || k16 != 0);
+            const uint32_t e_local = smem_u32(&empty[slot]);
+            tc_commit_2sm(e_local);
+            tc_commit_2sm(mapa_shared(e_local, 1));
+            issued = true;
+          }
+          if (ok) {
+            const uint32_t f_local = smem_u32(&acc_full[buf]);
+            tc_commit_2sm(f_local);
+            tc_commit_2sm(mapa_shared(f_local, 1));
+          }
+        }
+      }
+      if (issued) {  // all MMAs complete before the tensor memory is freed
+        tc_commit_2sm(smem_u32(drain));
+        if (!mbar_wait_bounded(drain, 0, kWaitLimitNs)) atomicOr(a.status, kStatusTimeout);
+      }
+    }
+  } else {
+    // ------------------------------ epilogue (both CTAs) ------------------------------
+    const int q = warp & 3;
+    uint32_t* stage = epi + (warp - 2) * 32 * kPairEpiPitch;
+    int unit = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += npairs) {
+      const Tile w = tile_at(t);
+      for (int p0 = 0; p0 < nk; p0 += piece, ++unit) {
+        const int buf = unit & 1;
+        if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int r0 = rank * kPairHalf + 32 * q;   // this warp's first row of the tile
+        if (r0 < w.rows)
+          pair_store<F32>(tmem_base + ((uint32_t)(32 * q) << 16) + buf * 256, stage, lane, a.out,
+                          (size_t)w.row0 + r0, w.rows - r0, w.n0, a.Ncols, false, p0 > 0);
+        tc_fence_before();
+        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_2sm(tmem_base, 512);
+}
+
+// Weight gradient.  Tile: 256 x 256 of dW[e]; the reduction runs over e's rows, 64 per stage,
+// from x [R, M] and dy [R, Ncols] as they lie (both MN-major: 64 x 64 boxes).  A segment's last
+// stage may hold rows of the next expert: a warp of each CTA overwrites them with zeros in both
+// operands (zeroing one would let a NaN or an infinity of the other through) before the MMAs
+// read them, up to the next multiple of 16; the MMAs stop there.  Such a stage's copies complete
+// on a barrier of their own CTA, and its `full` phase completes when both CTAs have masked.
+// Experts without rows get zeros.
+template <bool F32>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
+    grouped_wgrad_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap xmap,
+                         const __grid_constant__ CUtensorMap dymap) {
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ Segments seg;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  uint8_t* ring = align1k(smem_raw);
+  uint64_t* full = reinterpret_cast<uint64_t*>(ring + kPairStages * kPairStageBytes);
+  uint64_t* empty = full + kPairStages;
+  uint64_t* ragged = empty + kPairStages;   // this CTA's copies of a stage that gets masked
+  uint64_t* acc_full = ragged + kPairStages;
+  uint64_t* acc_empty = acc_full + 2;
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* epi = reinterpret_cast<uint32_t*>(ring + kPairStages * kPairStageBytes + 256);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = (int)cluster_ctarank();
+  const bool leader = rank == 0;
+
+  if (warp == 1) {
+    tmem_alloc_2sm(&s_tmem, 512);
+    tmem_relinquish_2sm();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < kPairStages; ++s) {
+      mbar_init(&full[s], 2);     // one arrival of each CTA (its producer's, or its masking warp's)
+      mbar_init(&empty[s], 1);
+      mbar_init(&ragged[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * 128);
+    }
+    mbar_init(drain, 1);
+    s_abort = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&xmap);
+    tma_prefetch_desc(&dymap);
+  }
+  pdl_wait();  // offsets and rows may come from the previous kernels
+  pdl_launch_next();
+  load_segments(seg, a.offsets, a.E, a.R, 1, a.status);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem;
+
+  const int NT = (a.Ncols + 255) / 256, MT = (a.M + 255) / 256;
+  const int per = NT * MT, tiles = a.E * per;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  volatile int* abort_flag = &s_abort;
+
+  if (warp == 0) {
+    // ------------------------------ TMA producer (both CTAs) ------------------------------
+    if (lane == 0) {
+      uint32_t it = 0, ragged_ph = 0;   // bit s: parity of the next masked stage in slot s
+      uint32_t last_ragged = 0;         // bit s: slot s's last stage was a masked one
+      int last_it[kPairStages];
+#pragma unroll
+      for (int s = 0; s < kPairStages; ++s) last_it[s] = -1;
+      for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+        const int e = t / per, l = t - e * per;
+        const int m0 = l / NT * 256 + rank * kPairHalf, n0 = l % NT * 256 + rank * kPairHalf;
+        const int beg = seg.beg[e], cnt = seg.cnt[e];
+        bool ok = true;
+        for (int r = 0; r < cnt; r += kGrBK, ++it) {
+          const int slot = it % kPairStages;
+          if (!wait_or_abort(&empty[slot], ((it / kPairStages) & 1u) ^ 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = ring + slot * kPairStageBytes;
+          constexpr int kBox = 64 * kGrBK * 2;
+          if (cnt - r >= kGrBK) {
+            const uint32_t bar = mapa_shared(smem_u32(&full[slot]), 0);
+            if (leader) mbar_arrive_expect_tx(&full[slot], 2 * kPairStageBytes);
+            else mbar_arrive_cluster(bar);
+            tma_load_2d_pair(st, &xmap, m0, beg + r, bar);
+            tma_load_2d_pair(st + kBox, &xmap, m0 + 64, beg + r, bar);
+            tma_load_2d_pair(st + 2 * kBox, &dymap, n0, beg + r, bar);
+            tma_load_2d_pair(st + 3 * kBox, &dymap, n0 + 64, beg + r, bar);
+            last_ragged &= ~(1u << slot);
+          } else {
+            mbar_arrive_expect_tx(&ragged[slot], kPairStageBytes);
+            tma_load_2d(st, &xmap, m0, beg + r, &ragged[slot]);
+            tma_load_2d(st + kBox, &xmap, m0 + 64, beg + r, &ragged[slot]);
+            tma_load_2d(st + 2 * kBox, &dymap, n0, beg + r, &ragged[slot]);
+            tma_load_2d(st + 3 * kBox, &dymap, n0 + 64, beg + r, &ragged[slot]);
+            last_ragged |= 1u << slot;
+            ragged_ph ^= 1u << slot;
+          }
+          last_it[slot] = it;
+        }
+        if (!ok) break;
+      }
+      // drain: a masked stage's copies are this CTA's own, the others are counted on the even
+      // CTA's full barriers
+      for (int s = 0; s < kPairStages; ++s) {
+        if (last_it[s] < 0) continue;
+        bool done = true;
+        if ((last_ragged >> s) & 1u)
+          done = mbar_wait_bounded(&ragged[s], ((ragged_ph >> s) & 1u) ^ 1u, kWaitLimitNs);
+        if (leader)
+          done = mbar_wait_bounded(&full[s], (last_it[s] / kPairStages) & 1u, kWaitLimitNs) && done;
+        if (!done) atomicOr(a.status, kStatusTimeout);
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------ MMA issuer (even CTA) ------------------------------
+    if (leader && lane == 0) {
+      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, true, true);
+      const uint32_t ring_s = smem_u32(ring);
+      const uint64_t adesc0 = smem_desc_sw128(ring_s, 64 * kGrBK * 2, 1024);
+      const uint64_t bdesc0 = smem_desc_sw128(ring_s + kPairABytes, 64 * kGrBK * 2, 1024);
+      uint32_t it = 0;
+      int unit = 0;
+      bool issued = false, ok = true;
+      for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
+        const int cnt = seg.cnt[t / per];
+        const int piece = F32 ? kGrPieceStages * kGrBK : max(cnt, 1);
+        for (int p0 = 0; ok && p0 < cnt; p0 += piece, ++unit) {
+          const int p1 = min(cnt, p0 + piece);
+          const int buf = unit & 1;
+          if (!wait_or_abort(&acc_empty[buf], ((unit >> 1) & 1u) ^ 1u, abort_flag, a.status)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem_base + buf * 256;
+          for (int r = p0; r < p1; r += kGrBK, ++it) {
+            const int slot = it % kPairStages;
+            if (!wait_or_abort_cluster(&full[slot], (it / kPairStages) & 1u, abort_flag,
+                                       a.status)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t soff = (uint64_t)((slot * kPairStageBytes) >> 4);
+            const int steps = min(kGrBK / 16, (cnt - r + 15) / 16);
+            for (int k16 = 0; k16 < steps; ++k16)
+              tc_mma_bf16_2sm(d, adesc0 + soff + ((k16 * 2048) >> 4),
+                              bdesc0 + soff + ((k16 * 2048) >> 4), idesc, r != p0 || k16 != 0);
+            const uint32_t e_local = smem_u32(&empty[slot]);
+            tc_commit_2sm(e_local);
+            tc_commit_2sm(mapa_shared(e_local, 1));
+            issued = true;
+          }
+          if (ok) {
+            const uint32_t f_local = smem_u32(&acc_full[buf]);
+            tc_commit_2sm(f_local);
+            tc_commit_2sm(mapa_shared(f_local, 1));
+          }
+        }
+      }
+      if (issued) {  // all MMAs complete before the tensor memory is freed
+        tc_commit_2sm(smem_u32(drain));
+        if (!mbar_wait_bounded(drain, 0, kWaitLimitNs)) atomicOr(a.status, kStatusTimeout);
+      }
+    }
+  } else if (warp == 6) {
+    // ------------------------------ masking of ragged ends (both CTAs) ------------------------
+    uint32_t it = 0, ragged_ph = 0;
+    for (int t = pair; t < tiles; t += npairs) {
+      const int cnt = seg.cnt[t / per], stages = (cnt + kGrBK - 1) / kGrBK, rem = cnt % kGrBK;
+      it += stages;
+      if (rem == 0) continue;
+      const int slot = (it - 1) % kPairStages;
+      if (!warp_wait(&ragged[slot], (ragged_ph >> slot) & 1u, abort_flag, a.status)) break;
+      ragged_ph ^= 1u << slot;
+      // a row of a 64 x 64 box is 128 contiguous bytes (the swizzle permutes inside them)
+      uint8_t* st = ring + slot * kPairStageBytes;
+      const int pad = (16 - rem % 16) % 16;
+      for (int i = lane; i < pad * 4 * 8; i += 32) {
+        const int box = i / (pad * 8), j = i % (pad * 8);
+        *reinterpret_cast<uint4*>(st + box * (64 * kGrBK * 2) + (rem + j / 8) * 128 + (j % 8) * 16) =
+            make_uint4(0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&full[slot]), 0));
+    }
+  } else {
+    // ------------------------------ epilogue (both CTAs) ------------------------------
+    const int q = warp & 3;
+    uint32_t* stage = epi + (warp - 2) * 32 * kPairEpiPitch;
+    int unit = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += npairs) {
+      const int e = t / per, l = t - e * per;
+      const int m0 = l / NT * 256 + rank * kPairHalf + 32 * q, n0 = l % NT * 256;
+      const int cnt = seg.cnt[e];
+      const int piece = F32 ? kGrPieceStages * kGrBK : max(cnt, 1);
+      const size_t row0 = (size_t)e * a.M + m0;
+      if (cnt == 0) {
+        if (m0 < a.M) pair_store<F32>(0, stage, lane, a.out, row0, a.M - m0, n0, a.Ncols, true, false);
+        continue;
+      }
+      for (int p0 = 0; p0 < cnt; p0 += piece, ++unit) {
+        const int buf = unit & 1;
+        if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (m0 < a.M)
+          pair_store<F32>(tmem_base + ((uint32_t)(32 * q) << 16) + buf * 256, stage, lane, a.out,
+                          row0, a.M - m0, n0, a.Ncols, false, p0 > 0);
+        tc_fence_before();
+        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_2sm(tmem_base, 512);
+}
+
+}  // namespace moe

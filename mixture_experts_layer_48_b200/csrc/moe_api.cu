@@ -10,7 +10,9 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <new>
+#include <type_traits>
 #include <utility>
 #include <vector>
 
@@ -24,6 +26,8 @@
 #include "expert_gemm.cuh"
 #include "expert_gemm_mx.cuh"
 #include "ep.cuh"
+#include "grouped.cuh"
+#include "rows.cuh"
 
 using namespace moe;
 
@@ -47,6 +51,8 @@ constexpr int kMxStreamT = 176;
 constexpr int kMaxKernelsPerCall = 12;
 
 moe_status static_scratch_address(void** out);  // defined beside the array, at the end
+bool set_rows_smem_attrs();                     // rows_api.cuh
+bool query_clusters(int num_sms, int* out);     // rows_api.cuh
 
 // Profiled kernel kinds (moe_profile_end): one per kernel family and projection.
 enum Kind { kKindRouter = 0, kKindRouteFin = 1, kKindGather = 2, kKindGateUp = 3,
@@ -87,6 +93,8 @@ struct moe_ctx {
   uint32_t* d_status = nullptr;
   cudaStream_t aux = nullptr;            // second stream for a call whose families fork
   cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
+  // clusters of 2, 4 and 8 one-CTA-per-SM blocks that run at the same time (grouped products)
+  int max_clusters[3] = {0, 0, 0};
   void* static_scratch = nullptr;  // device address of the routing scratch array (moe_route_static)
   uint64_t launches = 0;
   // profiling
@@ -634,6 +642,7 @@ bool set_smem_attrs() {
   ok &= cudaFuncSetAttribute(build_segment_lists_kernel,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (4 * kMaxSegments + 2 * kMaxE) * 4) == cudaSuccess;
+  ok &= set_rows_smem_attrs();
   return ok;
 }
 
@@ -1048,6 +1057,11 @@ moe_status moe_create(int E, int H, int I, int k, moe_t* out) {
   c->device = dev;
   c->num_sms = prop.multiProcessorCount;
   c->stream_T = default_stream_T(c);
+  if (!query_clusters(c->num_sms, c->max_clusters)) {
+    cudaGetLastError();
+    delete c;
+    return MOE_ERR_CUDA;
+  }
   // row-tile width of the grouped GEMM: MOE_ROW_TILE=512 or 256 (default below)
   if (const char* v = getenv("MOE_ROW_TILE")) c->wide_rows = strcmp(v, "512") == 0;
   // rows per expert tile: MOE_TILE_ROWS=128 or 256 (default: by each call's mean load)
@@ -1573,3 +1587,6 @@ moe_status moe_route_static(moe_t c, int T, const void* x_bf16, const void* W_ro
 }
 
 }  // extern "C"
+
+// The operators around the layer: grouped products, SwiGLU rows, block norms.
+#include "rows_api.cuh"

@@ -1,0 +1,397 @@
+// Row-wise operators around the expert products, all bound by HBM: SwiGLU on rows [gate | up]
+// with its backward pass, and the RMS norms before and after the block fused with its gate and
+// residual scale, with their backward pass.
+//
+// One row is spread over TPR threads, VPT vectors of 4 (or 8) consecutive elements each, and
+// stays in registers between the passes over it, so every input is read once and every output
+// written once.  All arithmetic and every sum is fp32.  Sums over rows (the gradients of the
+// norm weights and the gate) are kept in registers per thread over all rows of a persistent
+// block, written as one partial row per row group and added in a fixed order by a second kernel:
+// results do not depend on timing.
+#pragma once
+
+#include "common.cuh"
+#include "grouped.cuh"
+
+namespace moe {
+
+MOE_DEVINL float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+MOE_DEVINL float4 load4(const uint16_t* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16lo(v.x), bf16hi(v.x), bf16lo(v.y), bf16hi(v.y));
+}
+MOE_DEVINL void save4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+MOE_DEVINL void save4(uint16_t* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
+}
+// v as the type of p holds it.
+MOE_DEVINL float4 as_stored(const float*, float4 v) { return v; }
+MOE_DEVINL float4 as_stored(const uint16_t*, float4 v) {
+  const uint32_t a = cvt_bf16x2(v.x, v.y), b = cvt_bf16x2(v.z, v.w);
+  return make_float4(bf16lo(a), bf16hi(a), bf16lo(b), bf16hi(b));
+}
+
+MOE_DEVINL float4 operator*(float4 a, float4 b) {
+  return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
+MOE_DEVINL float4 operator*(float4 a, float b) { return make_float4(a.x * b, a.y * b, a.z * b, a.w * b); }
+MOE_DEVINL float4 fma4(float4 a, float4 b, float4 c) {
+  return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z),
+                     fmaf(a.w, b.w, c.w));
+}
+MOE_DEVINL float4 fma4(float4 a, float b, float4 c) {
+  return make_float4(fmaf(a.x, b, c.x), fmaf(a.y, b, c.y), fmaf(a.z, b, c.z), fmaf(a.w, b, c.w));
+}
+MOE_DEVINL float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
+
+// Sum over the TPR threads of a row, the same value in each of them.  `red` has a word per warp
+// of the block; every thread of the block takes part.  Two calls in a row alternate `red`.
+template <int TPR>
+MOE_DEVINL float row_sum(float v, float* red) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) red[warp] = v;
+    __syncthreads();
+    const float* mine = red + warp / W * W;
+    v = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) v += mine[i];
+  }
+  return v;
+}
+
+template <int TPR>
+struct RowCfg {
+  static constexpr int kThreads = TPR < 128 ? 128 : TPR;
+  static constexpr int kRows = kThreads / TPR;   // rows per block
+};
+
+// ---- norms around the block ---------------------------------------------------------------------
+struct NormArgs {
+  int T, H;
+  float eps, scale;
+  const void *resid, *y;                    // y null: no block output to add
+  const float *w_post, *gate, *w_next;      // null: no norm after / no gate / no norm before
+  void* resid_out;
+  uint16_t* x;
+  float *rstd_post, *rstd_next;             // forward: written
+  // backward
+  const void* dresid;                       // null: nothing flows into the new residual itself
+  const uint16_t* dx;
+  const float *c_rstd_post, *c_rstd_next;
+  void *dresid_out, *dy;
+  int dy_f32;
+  float *part_y, *part_x;                   // [row groups, H] partial column sums, or null
+};
+
+// r' = r + scale * gate * norm(y);  x = norm(r').  RT, YT: float or uint16_t (bf16).
+template <int TPR, int VPT, typename RT, typename YT>
+__global__ void __launch_bounds__(RowCfg<TPR>::kThreads)
+    block_norm_kernel(const NormArgs a) {
+  constexpr int kRows = RowCfg<TPR>::kRows;
+  __shared__ float red[2][RowCfg<TPR>::kThreads / 32];
+  const int lane = threadIdx.x % TPR;
+  const int t = blockIdx.x * kRows + threadIdx.x / TPR;
+  const bool live = t < a.T;
+  const int nv = live ? a.H / 4 : 0;
+  const size_t base = (size_t)t * a.H;
+  pdl_wait();
+  pdl_launch_next();
+  const RT* resid = static_cast<const RT*>(a.resid) + base;
+  const YT* yrow = static_cast<const YT*>(a.y) + base;
+  const float inv_h = 1.f / (float)a.H;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 r[VPT], y[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * TPR + lane;
+    r[i] = v < nv ? load4(resid + 4 * v) : zero;
+  }
+  if (a.y != nullptr) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * TPR + lane;
+      y[i] = v < nv ? load4(yrow + 4 * v) : zero;
+    }
+    float s = 1.f;
+    if (a.w_post != nullptr) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) ss += dot4(y[i], y[i]);
+      s = rsqrtf(row_sum<TPR>(ss, red[0]) * inv_h + a.eps);
+      if (live && lane == 0) a.rstd_post[t] = s;
+    }
+    RT* out = static_cast<RT*>(a.resid_out) + base;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * TPR + lane;
+      if (v < nv) {
+        float4 n = y[i];
+        if (a.w_post != nullptr) n = n * s * load4(a.w_post + 4 * v);
+        if (a.gate != nullptr) n = n * load4(a.gate + 4 * v);
+        const float4 q = fma4(n, a.scale, r[i]);
+        save4(out + 4 * v, q);
+        r[i] = as_stored(out, q);   // the next norm reads what a reader of r' would
+      }
+    }
+  }
+  if (a.x != nullptr) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) ss += dot4(r[i], r[i]);
+    const float s = rsqrtf(row_sum<TPR>(ss, red[1]) * inv_h + a.eps);
+    if (live && lane == 0) a.rstd_next[t] = s;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * TPR + lane;
+      if (v < nv) save4(a.x + base + 4 * v, r[i] * s * load4(a.w_next + 4 * v));
+    }
+  }
+}
+
+// Backward.  With rh = r' * rstd_next and t = dx * w_next:
+//   dr = dresid + rstd_next * (t - rh * mean(t * rh))                 gradient of r' and of r
+// with yh = y * rstd_post (or y without the norm after) and d = scale * gate * dr * w_post:
+//   dy = rstd_post * (d - yh * mean(d * yh))                          (or scale * gate * dr)
+// column sums: part_x = sum dx * rh (dw_next), part_y = sum dr * yh (dw_post and dgate follow).
+template <int TPR, int VPT, typename RT, typename YT>
+__global__ void __launch_bounds__(RowCfg<TPR>::kThreads, TPR <= 128 ? 3 : 1)
+    block_norm_backward_kernel(const NormArgs a) {
+  constexpr int kRows = RowCfg<TPR>::kRows;
+  __shared__ float red[2][RowCfg<TPR>::kThreads / 32];
+  const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const float inv_h = 1.f / (float)a.H;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 sum_x[VPT], sum_y[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) sum_x[i] = sum_y[i] = zero;
+  pdl_wait();
+  pdl_launch_next();
+  // every thread of the block takes every step (the row sums are block-wide)
+  for (int t0 = blockIdx.x * kRows; t0 < a.T; t0 += gridDim.x * kRows) {
+    const int t = t0 + sub;
+    const bool live = t < a.T;
+    const int nv = live ? a.H / 4 : 0;
+    const size_t base = (size_t)t * a.H;
+    float4 dr[VPT], dx[VPT], r[VPT], y[VPT];
+    const RT* dres = static_cast<const RT*>(a.dresid) + base;
+    const RT* res = static_cast<const RT*>(a.resid) + base;
+    const YT* yrow = static_cast<const YT*>(a.y) + base;
+    const bool need_y = a.y != nullptr;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * TPR + lane;
+      dr[i] = a.dresid != nullptr && v < nv ? load4(dres + 4 * v) : zero;
+    }
+    if (a.dx != nullptr) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + lane;
+        dx[i] = v < nv ? load4(a.dx + base + 4 * v) : zero;
+        r[i] = v < nv ? load4(res + 4 * v) : zero;
+      }
+    }
+    if (need_y) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + lane;
+        y[i] = v < nv ? load4(yrow + 4 * v) : zero;
+      }
+    }
+    if (a.dx != nullptr) {
+      const float s = live ? a.c_rstd_next[t] : 0.f;
+      float c = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + lane;
+        if (v < nv) {
+          r[i] = r[i] * s;
+          sum_x[i] = fma4(dx[i], r[i], sum_x[i]);
+          dx[i] = dx[i] * load4(a.w_next + 4 * v);
+          c += dot4(dx[i], r[i]);
+        }
+      }
+      c = row_sum<TPR>(c, red[0]) * inv_h;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) dr[i] = fma4(fma4(r[i], -c, dx[i]), s, dr[i]);
+    }
+    RT* out = static_cast<RT*>(a.dresid_out) + base;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * TPR + lane;
+      if (v < nv) save4(out + 4 * v, dr[i]);
+    }
+    if (a.dy != nullptr) {
+      const float s = a.w_post != nullptr && live ? a.c_rstd_post[t] : 1.f;
+      float c = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + lane;
+        if (v < nv) {
+          if (need_y) {
+            y[i] = y[i] * s;
+            sum_y[i] = fma4(dr[i], y[i], sum_y[i]);
+          }
+          dr[i] = dr[i] * a.scale;
+          if (a.gate != nullptr) dr[i] = dr[i] * load4(a.gate + 4 * v);
+          if (a.w_post != nullptr) {
+            dr[i] = dr[i] * load4(a.w_post + 4 * v);
+            c += dot4(dr[i], y[i]);
+          }
+        }
+      }
+      if (a.w_post != nullptr) {
+        c = row_sum<TPR>(c, red[1]) * inv_h;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) dr[i] = fma4(y[i], -c, dr[i]) * s;
+      }
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = i * TPR + lane;
+        if (v < nv) {
+          if (a.dy_f32) save4(static_cast<float*>(a.dy) + base + 4 * v, dr[i]);
+          else save4(static_cast<uint16_t*>(a.dy) + base + 4 * v, dr[i]);
+        }
+      }
+    }
+    // the next row's first row_sum must not overwrite words that a slower warp still reads:
+    // a row that takes one sum has no second barrier in between
+    if (TPR > 32) __syncthreads();
+  }
+  const size_t row = (size_t)(blockIdx.x * kRows + sub) * a.H;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * TPR + lane;
+    if (v < a.H / 4) {
+      if (a.part_x != nullptr) save4(a.part_x + row + 4 * v, sum_x[i]);
+      if (a.part_y != nullptr) save4(a.part_y + row + 4 * v, sum_y[i]);
+    }
+  }
+}
+
+// dw_next[h] = sum_p part_x[p, h]; with S[h] = sum_p part_y[p, h]: dw_post = scale * gate * S and
+// dgate = scale * w_post * S.  block 256 = 32 columns x 8 slices of the partial rows, each slice
+// added in row order, then the slices in order.  grid (ceil(H / 32), 2).
+__global__ void __launch_bounds__(256)
+    block_norm_colsum_kernel(const float* __restrict__ part_x, const float* __restrict__ part_y,
+                             int parts, int H, float scale, const float* __restrict__ gate,
+                             const float* __restrict__ w_post, float* __restrict__ dw_next,
+                             float* __restrict__ dw_post, float* __restrict__ dgate) {
+  __shared__ float acc[8][33];
+  pdl_wait();
+  pdl_launch_next();
+  const float* part = blockIdx.y == 0 ? part_x : part_y;
+  if (part == nullptr) return;
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int h = blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (h < H) {
+    const int per = (parts + 7) / 8, p1 = min(parts, (slice + 1) * per);
+#pragma unroll 8
+    for (int p = slice * per; p < p1; ++p) s += part[(size_t)p * H + h];
+  }
+  acc[slice][lane] = s;
+  __syncthreads();
+  if (slice != 0 || h >= H) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += acc[i][lane];
+  if (blockIdx.y == 0) {
+    dw_next[h] = s;
+    return;
+  }
+  s *= scale;
+  if (dw_post != nullptr) dw_post[h] = gate != nullptr ? s * gate[h] : s;
+  if (dgate != nullptr) dgate[h] = w_post != nullptr ? s * w_post[h] : s;
+}
+
+// ---- SwiGLU on rows [gate | up] -----------------------------------------------------------------
+MOE_DEVINL float sigmoid_f32(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+
+// h[r, :] = row_w[r] * silu(gu[r, :I]) * gu[r, I:] (row_w null: 1).  One thread per 8 elements.
+__global__ void __launch_bounds__(256)
+    swiglu_rows_kernel(const uint16_t* __restrict__ gu, const float* __restrict__ row_w,
+                       uint16_t* __restrict__ h, int R, int I) {
+  pdl_wait();
+  pdl_launch_next();
+  const int nv = I / 8;
+  const long long n = (long long)R * nv;
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) {
+    const int r = (int)(i / nv), v = (int)(i - (long long)r * nv);
+    const uint16_t* row = gu + (size_t)r * 2 * I + 8 * v;
+    const uint4 g = *reinterpret_cast<const uint4*>(row);
+    const uint4 u = *reinterpret_cast<const uint4*>(row + I);
+    const float w = row_w != nullptr ? row_w[r] : 1.f;
+    auto one = [&](uint32_t a, uint32_t b) {
+      const float g0 = bf16lo(a), g1 = bf16hi(a);
+      return cvt_bf16x2(w * (g0 * sigmoid_f32(g0) * bf16lo(b)), w * (g1 * sigmoid_f32(g1) * bf16hi(b)));
+    };
+    *reinterpret_cast<uint4*>(h + (size_t)r * I + 8 * v) =
+        make_uint4(one(g.x, u.x), one(g.y, u.y), one(g.z, u.z), one(g.w, u.w));
+  }
+}
+
+// With s = sigmoid(g): du = w dh g s;  dg = w dh u s (1 + g (1 - s));  dw = sum dh g s u.
+template <int TPR, int VPT>
+__global__ void __launch_bounds__(RowCfg<TPR>::kThreads)
+    swiglu_rows_backward_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu,
+                                const float* __restrict__ row_w, uint16_t* __restrict__ dgu,
+                                float* __restrict__ drow_w, int R, int I) {
+  constexpr int kRows = RowCfg<TPR>::kRows;
+  __shared__ float red[RowCfg<TPR>::kThreads / 32];
+  const int lane = threadIdx.x % TPR;
+  const int r = blockIdx.x * kRows + threadIdx.x / TPR;
+  const bool live = r < R;
+  const int nv = live ? I / 8 : 0;
+  pdl_wait();
+  pdl_launch_next();
+  const uint16_t* drow = dh + (size_t)r * I;
+  const uint16_t* row = gu + (size_t)r * 2 * I;
+  uint4 d[VPT], g[VPT], u[VPT];
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * TPR + lane;
+    d[i] = v < nv ? *reinterpret_cast<const uint4*>(drow + 8 * v) : zero;
+    g[i] = v < nv ? *reinterpret_cast<const uint4*>(row + 8 * v) : zero;
+    u[i] = v < nv ? *reinterpret_cast<const uint4*>(row + I + 8 * v) : zero;
+  }
+  const float w = row_w != nullptr && live ? row_w[r] : 1.f;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * TPR + lane;
+    if (v >= nv) continue;
+    uint32_t* dp = reinterpret_cast<uint32_t*>(&d[i]);
+    uint32_t* gp = reinterpret_cast<uint32_t*>(&g[i]);
+    uint32_t* up = reinterpret_cast<uint32_t*>(&u[i]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float dg[2], du[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float dd = k ? bf16hi(dp[j]) : bf16lo(dp[j]);
+        const float gg = k ? bf16hi(gp[j]) : bf16lo(gp[j]);
+        const float uu = k ? bf16hi(up[j]) : bf16lo(up[j]);
+        const float s = sigmoid_f32(gg), a = gg * s;
+        sum = fmaf(dd * uu, a, sum);
+        const float wd = w * dd;
+        du[k] = wd * a;
+        dg[k] = wd * uu * fmaf(a, 1.f - s, s);
+      }
+      gp[j] = cvt_bf16x2(dg[0], dg[1]);
+      up[j] = cvt_bf16x2(du[0], du[1]);
+    }
+    uint16_t* out = dgu + (size_t)r * 2 * I + 8 * v;
+    *reinterpret_cast<uint4*>(out) = g[i];
+    *reinterpret_cast<uint4*>(out + I) = u[i];
+  }
+  if (drow_w != nullptr) {
+    sum = row_sum<TPR>(sum, red);
+    if (live && lane == 0) drow_w[r] = sum;
+  }
+}
+
+}  // namespace moe

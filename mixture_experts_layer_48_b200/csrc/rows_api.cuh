@@ -1,0 +1,441 @@
+// Host side of the operators around the layer (include/moe.h, "Training and the block around the
+// layer"): argument checks, kernel variants and launches.  Included once, by moe_api.cu, whose
+// handle, launch helpers and TMA encoder it uses.
+#pragma once
+
+namespace {
+
+constexpr int kMaxKN = 32768;         // K and N of the grouped products (gate/up: N = 2I)
+constexpr int kMaxRows = 1 << 28;     // rows of one call
+constexpr int kColsSmallRows = 32;    // rows per tile of the few-row kernels
+constexpr int kColsRows = 128;
+
+bool on_device(const moe_ctx* c) {
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return false;
+  }
+  return dev == c->device;
+}
+
+bool all_aligned16(std::initializer_list<const void*> ps) {  // null passes
+  for (const void* p : ps)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
+// bf16 rows [rows, cols], or planes [planes, rows, cols], with a [box_rows, 64] box and the
+// 128-byte swizzle.  Encoded for every call: the map holds nothing but the call's own arguments.
+bool encode_rows(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+  return encode_2d(m, base, rows, cols, box_rows, kGrBK, CU_TENSOR_MAP_SWIZZLE_128B, true);
+}
+bool encode_planes(CUtensorMap* m, const void* base, uint64_t planes, uint64_t rows, uint64_t cols,
+                   uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {cols, rows, planes};
+  cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
+  cuuint32_t box[3] = {(cuuint32_t)kGrBK, box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launch with programmatic dependent launch on clusters of `cluster` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                               int cluster, cudaStream_t st, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename K>
+bool smem_attr(K kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+         cudaSuccess;
+}
+
+template <bool TRANS, bool F32>
+bool set_grouped_attrs() {
+  return smem_attr(grouped_cols_kernel<kColsSmallRows, 1, TRANS, F32>,
+                   ColsCfg<kColsSmallRows, 1>::kSmem) &&
+         smem_attr(grouped_cols_kernel<kColsRows, 1, TRANS, F32>, ColsCfg<kColsRows, 1>::kSmem) &&
+         smem_attr(grouped_cols_kernel<kColsRows, 2, TRANS, F32>, ColsCfg<kColsRows, 2>::kSmem) &&
+         smem_attr(grouped_rows_kernel<TRANS, F32>, kPairSmem);
+}
+
+bool set_rows_smem_attrs() {
+  return set_grouped_attrs<false, false>() && set_grouped_attrs<false, true>() &&
+         set_grouped_attrs<true, false>() && set_grouped_attrs<true, true>() &&
+         smem_attr(grouped_wgrad_kernel<false>, kPairSmem) &&
+         smem_attr(grouped_wgrad_kernel<true>, kPairSmem);
+}
+
+// Clusters of 2, 4 and 8 CTAs of the few-row kernel (one CTA per SM) that fit the GPU at once: a
+// cluster lies inside one GPC, whose SM count need not be a multiple of its size.
+bool query_clusters(int num_sms, int* out) {
+  for (int i = 0; i < 3; ++i) {
+    const int size = 2 << i;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms / size * size);
+    cfg.blockDim = dim3(kColsThreads);
+    cfg.dynamicSmemBytes = ColsCfg<kColsSmallRows, 1>::kSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&out[i], grouped_cols_kernel<kColsSmallRows, 1, false, false>,
+                                       &cfg) != cudaSuccess ||
+        out[i] < 1)
+      return false;
+  }
+  return true;
+}
+
+// Which kernel multiplies a call's rows, from sizes the host knows (the segments stay on the
+// device).
+struct GroupedPlan {
+  enum Kind { kColsSmall, kCols, kColsWide, kRows } kind;
+  int split;    // CTAs per cluster that share a tile's reduction
+};
+
+GroupedPlan plan_grouped(const moe_ctx* c, int R, int Kred, int Ncols) {
+  const int nk = (Kred + kGrBK - 1) / kGrBK;
+  const long long mean = ((long long)R + c->E - 1) / c->E;
+  const long long busy = std::min(R, c->E);      // experts that can hold rows
+  auto tiles = [&](int rows, int cols) {
+    return busy * ((mean + rows - 1) / rows) * ((Ncols + cols - 1) / cols);
+  };
+  auto split_for = [&](long long n) {            // enough CTAs for about four waves of tiles
+    int s = 1;
+    while (s < 8 && n * s < 4ll * c->num_sms && nk >= 8 * s) s *= 2;
+    return s;
+  };
+  GroupedPlan p;
+  if (mean <= kColsSmallRows / 2) {
+    p.kind = GroupedPlan::kColsSmall;
+    p.split = split_for(tiles(kColsSmallRows, 128));
+  } else if (mean > 160 && tiles(256, 256) >= c->num_sms / 2) {
+    p.kind = GroupedPlan::kRows;
+    p.split = 1;
+  } else if (tiles(kColsRows, 256) >= 2ll * c->num_sms) {
+    p.kind = GroupedPlan::kColsWide;
+    p.split = 1;
+  } else {
+    p.kind = GroupedPlan::kCols;
+    p.split = split_for(tiles(kColsRows, 128));
+  }
+  return p;
+}
+
+template <int ROWS, int NM, bool TRANS, bool F32>
+cudaError_t launch_cols(const moe_ctx* c, int split, const GroupedArgs& a, const CUtensorMap& wmap,
+                        const CUtensorMap& xmap, cudaStream_t st) {
+  auto kernel = grouped_cols_kernel<ROWS, NM, TRANS, F32>;
+  const size_t smem = ColsCfg<ROWS, NM>::kSmem;
+  const int clusters = split == 1 ? c->num_sms : c->max_clusters[split / 4];  // 2, 4, 8 -> 0, 1, 2
+  return launch_pdl_cluster(kernel, dim3(clusters * split), dim3(kColsThreads), smem, split, st, a,
+                            wmap, xmap, split);
+}
+
+template <bool TRANS, bool F32>
+moe_status run_grouped(moe_ctx* c, const GroupedArgs& a, const void* W, const void* x, int K, int N,
+                       cudaStream_t st) {
+  const GroupedPlan p = plan_grouped(c, a.R, a.Kred, a.Ncols);
+  const bool rows = p.kind == GroupedPlan::kRows;
+  CUtensorMap wmap, xmap;
+  // transposed: boxes of 128 weight rows (columns of the result) x 64; else 64 x 64
+  if (!encode_planes(&wmap, W, c->E, K, N, TRANS ? 128 : kGrBK) ||
+      !encode_rows(&xmap, x, a.R, a.Kred, rows ? kPairHalf : kColsRowBox))
+    return MOE_ERR_CUDA;
+  return launch(c, -1, st, [&] {
+    switch (p.kind) {
+      case GroupedPlan::kColsSmall:
+        return launch_cols<kColsSmallRows, 1, TRANS, F32>(c, p.split, a, wmap, xmap, st);
+      case GroupedPlan::kCols:
+        return launch_cols<kColsRows, 1, TRANS, F32>(c, p.split, a, wmap, xmap, st);
+      case GroupedPlan::kColsWide:
+        return launch_cols<kColsRows, 2, TRANS, F32>(c, p.split, a, wmap, xmap, st);
+      default:
+        return launch_pdl(grouped_rows_kernel<TRANS, F32>, dim3(c->num_sms / 2 * 2),
+                          dim3(kPairThreads), (size_t)kPairSmem, st, a, wmap, xmap);
+    }
+  });
+}
+
+bool grouped_shape_ok(const moe_ctx* c, int R, int K, int N, moe_dtype out_type) {
+  return R >= 0 && R <= kMaxRows && K >= 8 && K <= kMaxKN && K % 8 == 0 && N >= 8 && N <= kMaxKN &&
+         N % 8 == 0 && (out_type == MOE_BF16 || out_type == MOE_F32);
+}
+
+// ---- row kernels: threads per row from the row's length ------------------------------------------
+// f<TPR, VPT4>(): TPR threads hold VPT4 vectors of 4 elements each of a row of n elements.
+// 6 vectors keep a row of 2880 on 128 threads at 94 % use, with every load of the row in flight.
+template <typename F>
+moe_status by_row_length(int n, F&& f) {
+  using std::integral_constant;
+  if (n <= 24 * 32) return f(integral_constant<int, 32>{}, integral_constant<int, 6>{});
+  if (n <= 24 * 64) return f(integral_constant<int, 64>{}, integral_constant<int, 6>{});
+  if (n <= 24 * 128) return f(integral_constant<int, 128>{}, integral_constant<int, 6>{});
+  if (n <= 24 * 256) return f(integral_constant<int, 256>{}, integral_constant<int, 6>{});
+  if (n <= 24 * 512) return f(integral_constant<int, 512>{}, integral_constant<int, 6>{});
+  return f(integral_constant<int, 512>{}, integral_constant<int, 8>{});
+}
+
+template <typename F>
+moe_status by_types(moe_dtype resid_type, moe_dtype y_type, F&& f) {
+  if (resid_type == MOE_F32)
+    return y_type == MOE_F32 ? f(float{}, float{}) : f(float{}, uint16_t{});
+  return y_type == MOE_F32 ? f(uint16_t{}, float{}) : f(uint16_t{}, uint16_t{});
+}
+
+bool dtype_ok(moe_dtype t) { return t == MOE_BF16 || t == MOE_F32; }
+
+// Persistent blocks of the backward norm: three fit an SM up to 128 threads a row (at most 170
+// registers a thread), else one.
+template <int TPR>
+int norm_backward_blocks(const moe_ctx* c, int T) {
+  const long long need = ((long long)T + RowCfg<TPR>::kRows - 1) / RowCfg<TPR>::kRows;
+  return (int)std::min<long long>(need, (long long)c->num_sms * (TPR <= 128 ? 3 : 1));
+}
+
+// Partial rows of each column sum.
+int norm_backward_parts(const moe_ctx* c, int T) {
+  int parts = 0;
+  by_row_length(c->H, [&](auto tpr, auto) {
+    constexpr int TPR = decltype(tpr)::value;
+    parts = norm_backward_blocks<TPR>(c, T) * RowCfg<TPR>::kRows;
+    return MOE_OK;
+  });
+  return parts;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status moe_grouped_matmul(moe_t c, int R, int K, int N, int transpose, const int32_t* offsets,
+                              const void* x_rows_bf16, const void* W_bf16, void* out,
+                              moe_dtype out_type, moe_stream_t stream) {
+  if (!c || !grouped_shape_ok(c, R, K, N, out_type)) return MOE_ERR_ARG;
+  if (R == 0) return MOE_OK;
+  if (!offsets || !x_rows_bf16 || !W_bf16 || !out) return MOE_ERR_ARG;
+  if (!all_aligned16({offsets, x_rows_bf16, W_bf16, out}) || !on_device(c)) return MOE_ERR_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  GroupedArgs a{};
+  a.offsets = offsets;
+  a.E = c->E;
+  a.R = R;
+  a.Kred = transpose ? N : K;
+  a.Ncols = transpose ? K : N;
+  a.out = out;
+  a.status = c->d_status;
+  if (transpose)
+    return out_type == MOE_F32 ? run_grouped<true, true>(c, a, W_bf16, x_rows_bf16, K, N, st)
+                               : run_grouped<true, false>(c, a, W_bf16, x_rows_bf16, K, N, st);
+  return out_type == MOE_F32 ? run_grouped<false, true>(c, a, W_bf16, x_rows_bf16, K, N, st)
+                             : run_grouped<false, false>(c, a, W_bf16, x_rows_bf16, K, N, st);
+}
+
+moe_status moe_grouped_wgrad(moe_t c, int R, int K, int N, const int32_t* offsets,
+                             const void* x_rows_bf16, const void* dy_rows_bf16, void* dW,
+                             moe_dtype out_type, moe_stream_t stream) {
+  if (!c || !grouped_shape_ok(c, R, K, N, out_type)) return MOE_ERR_ARG;
+  if (!dW || !aligned16(dW) || !on_device(c)) return MOE_ERR_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (R == 0) {
+    const size_t bytes = (size_t)c->E * K * N * (out_type == MOE_F32 ? 4 : 2);
+    return cudaMemsetAsync(dW, 0, bytes, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+  }
+  if (!offsets || !x_rows_bf16 || !dy_rows_bf16 ||
+      !all_aligned16({offsets, x_rows_bf16, dy_rows_bf16}))
+    return MOE_ERR_ARG;
+  GroupedArgs a{};
+  a.offsets = offsets;
+  a.E = c->E;
+  a.R = R;
+  a.Ncols = N;
+  a.M = K;
+  a.out = dW;
+  a.status = c->d_status;
+  CUtensorMap xmap, dymap;
+  if (!encode_rows(&xmap, x_rows_bf16, R, K, kGrBK) || !encode_rows(&dymap, dy_rows_bf16, R, N, kGrBK))
+    return MOE_ERR_CUDA;
+  return launch(c, -1, st, [&] {
+    return launch_pdl(out_type == MOE_F32 ? grouped_wgrad_kernel<true> : grouped_wgrad_kernel<false>,
+                      dim3(c->num_sms / 2 * 2), dim3(kWgradThreads), (size_t)kPairSmem, st, a, xmap,
+                      dymap);
+  });
+}
+
+moe_status moe_swiglu(moe_t c, int R, const void* gu_bf16, const float* row_w, void* h_bf16,
+                      moe_stream_t stream) {
+  if (!c || R < 0 || R > kMaxRows) return MOE_ERR_ARG;
+  if (R == 0) return MOE_OK;
+  if (!gu_bf16 || !h_bf16 || !all_aligned16({gu_bf16, row_w, h_bf16}) || !on_device(c))
+    return MOE_ERR_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const long long blocks = ((long long)R * (c->I / 8) + 255) / 256;
+  return launch(c, -1, st, [&] {
+    return launch_pdl(swiglu_rows_kernel, dim3((unsigned)std::min<long long>(blocks, 1 << 30)),
+                      dim3(256), 0, st, static_cast<const uint16_t*>(gu_bf16), row_w,
+                      static_cast<uint16_t*>(h_bf16), R, c->I);
+  });
+}
+
+moe_status moe_swiglu_backward(moe_t c, int R, const void* dh_bf16, const void* gu_bf16,
+                               const float* row_w, void* dgu_bf16, float* drow_w,
+                               moe_stream_t stream) {
+  if (!c || R < 0 || R > kMaxRows) return MOE_ERR_ARG;
+  if (R == 0) return MOE_OK;
+  if (!dh_bf16 || !gu_bf16 || !dgu_bf16 || (drow_w && !row_w) ||
+      !all_aligned16({dh_bf16, gu_bf16, row_w, dgu_bf16, drow_w}) || !on_device(c))
+    return MOE_ERR_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  return by_row_length(c->I, [&](auto tpr, auto vpt) {
+    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value / 2;
+    const int rows = RowCfg<TPR>::kRows;
+    return launch(c, -1, st, [&] {
+      return launch_pdl(swiglu_rows_backward_kernel<TPR, VPT>, dim3((R + rows - 1) / rows),
+                        dim3(RowCfg<TPR>::kThreads), 0, st, static_cast<const uint16_t*>(dh_bf16),
+                        static_cast<const uint16_t*>(gu_bf16), row_w,
+                        static_cast<uint16_t*>(dgu_bf16), drow_w, R, c->I);
+    });
+  });
+}
+
+moe_status moe_block_norm(moe_t c, int T, moe_dtype resid_type, moe_dtype y_type, const void* resid,
+                          const void* y, const float* w_post, const float* gate, float scale,
+                          const float* w_next, float eps, void* resid_out, void* x_bf16,
+                          float* rstd_post, float* rstd_next, moe_stream_t stream) {
+  if (!c || T < 0 || T > kMaxT || !dtype_ok(resid_type) || !dtype_ok(y_type)) return MOE_ERR_ARG;
+  if (!(eps > 0.f) || !std::isfinite(eps) || !std::isfinite(scale)) return MOE_ERR_ARG;
+  if (T == 0) return MOE_OK;
+  if (!resid || (y != nullptr) != (resid_out != nullptr)) return MOE_ERR_ARG;
+  if (!y && (w_post || gate || !w_next)) return MOE_ERR_ARG;
+  if ((w_post != nullptr) != (rstd_post != nullptr)) return MOE_ERR_ARG;
+  if ((w_next != nullptr) != (x_bf16 != nullptr) || (w_next != nullptr) != (rstd_next != nullptr))
+    return MOE_ERR_ARG;
+  if (!all_aligned16({resid, y, w_post, gate, w_next, resid_out, x_bf16, rstd_post, rstd_next}) ||
+      !on_device(c))
+    return MOE_ERR_ARG;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  NormArgs a{};
+  a.T = T;
+  a.H = c->H;
+  a.eps = eps;
+  a.scale = scale;
+  a.resid = resid;
+  a.y = y;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_next = w_next;
+  a.resid_out = resid_out;
+  a.x = static_cast<uint16_t*>(x_bf16);
+  a.rstd_post = rstd_post;
+  a.rstd_next = rstd_next;
+  return by_row_length(c->H, [&](auto tpr, auto vpt) {
+    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+    return by_types(resid_type, y_type, [&](auto rt, auto yt) {
+      const int rows = RowCfg<TPR>::kRows;
+      return launch(c, -1, st, [&] {
+        return launch_pdl(block_norm_kernel<TPR, VPT, decltype(rt), decltype(yt)>,
+                          dim3((T + rows - 1) / rows), dim3(RowCfg<TPR>::kThreads), 0, st, a);
+      });
+    });
+  });
+}
+
+size_t moe_block_norm_workspace_bytes(moe_t c, int T) {
+  if (!c || T < 0 || T > kMaxT) return 0;
+  // two partial sums (the norm before, the norm after and the gate) of H columns each
+  return 2 * sizeof(float) * (size_t)std::max(1, norm_backward_parts(c, T)) * c->H;
+}
+
+moe_status moe_block_norm_backward(moe_t c, int T, moe_dtype resid_type, moe_dtype y_type,
+                                   moe_dtype dy_type, const void* dresid, const void* dx_bf16,
+                                   const void* resid, const void* y, const float* rstd_post,
+                                   const float* rstd_next, const float* w_post, const float* gate,
+                                   float scale, const float* w_next, void* dresid_out, void* dy,
+                                   float* dw_post, float* dgate, float* dw_next, void* workspace,
+                                   size_t ws_bytes, moe_stream_t stream) {
+  if (!c || T < 0 || T > kMaxT || !dtype_ok(resid_type) || !dtype_ok(y_type) || !dtype_ok(dy_type))
+    return MOE_ERR_ARG;
+  if (!std::isfinite(scale)) return MOE_ERR_ARG;
+  const bool next = w_next != nullptr, post = w_post != nullptr, gated = gate != nullptr;
+  if (next != (dw_next != nullptr) || post != (dw_post != nullptr) || gated != (dgate != nullptr))
+    return MOE_ERR_ARG;
+  if (T > 0) {
+    if (next != (dx_bf16 != nullptr) || next != (rstd_next != nullptr) || (next && !resid))
+      return MOE_ERR_ARG;
+    if (post != (rstd_post != nullptr) || ((post || gated) && (!y || !dy))) return MOE_ERR_ARG;
+    if (!dresid_out || (!next && !dy) || (!next && !dresid)) return MOE_ERR_ARG;
+  }
+  if (!all_aligned16({dresid, dx_bf16, resid, y, rstd_post, rstd_next, w_post, gate, w_next,
+                      dresid_out, dy, dw_post, dgate, dw_next}) ||
+      !on_device(c))
+    return MOE_ERR_ARG;
+  const bool sums = next || post || gated;
+  if (sums && (!workspace || !aligned16(workspace) || ws_bytes < moe_block_norm_workspace_bytes(c, T)))
+    return MOE_ERR_WORKSPACE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int parts = norm_backward_parts(c, T);
+  float* part_x = next ? static_cast<float*>(workspace) : nullptr;
+  float* part_y = post || gated ? static_cast<float*>(workspace) + (size_t)parts * c->H : nullptr;
+  if (T > 0) {
+    NormArgs a{};
+    a.T = T;
+    a.H = c->H;
+    a.scale = scale;
+    a.resid = resid;
+    a.y = post || gated ? y : nullptr;
+    a.w_post = w_post;
+    a.gate = gate;
+    a.w_next = w_next;
+    a.dresid = dresid;
+    a.dx = static_cast<const uint16_t*>(dx_bf16);
+    a.c_rstd_post = rstd_post;
+    a.c_rstd_next = rstd_next;
+    a.dresid_out = dresid_out;
+    a.dy = dy;
+    a.dy_f32 = dy_type == MOE_F32;
+    a.part_x = part_x;
+    a.part_y = part_y;
+    MOE_TRY(by_row_length(c->H, [&](auto tpr, auto vpt) {
+      constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+      return by_types(resid_type, y_type, [&](auto rt, auto yt) {
+        return launch(c, -1, st, [&] {
+          return launch_pdl(block_norm_backward_kernel<TPR, VPT, decltype(rt), decltype(yt)>,
+                            dim3(norm_backward_blocks<TPR>(c, T)), dim3(RowCfg<TPR>::kThreads), 0,
+                            st, a);
+        });
+      });
+    }));
+  }
+  if (!sums) return MOE_OK;
+  return launch(c, -1, st, [&] {
+    return launch_pdl(block_norm_colsum_kernel, dim3((c->H + 31) / 32, 2), dim3(256), 0, st,
+                      (const float*)part_x, (const float*)part_y, parts, c->H, scale, gate, w_post,
+                      dw_next, dw_post, dgate);
+  });
+}
+
+}  // extern "C"
