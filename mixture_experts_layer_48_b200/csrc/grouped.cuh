@@ -8,7 +8,7 @@
 //   weight gradient    dW[e]   = sum_r x[r, :]^T dy[r, :]   over e's rows         [E, K, N]
 //
 // Three kernel shapes, all persistent and warp-specialised (TMA producer warp, MMA issuer warp,
-// four epilogue warps) around a ring of 128-byte-swizzled shared-memory stages of 64 reduction
+// four or eight epilogue warps) around a ring of 128-byte-swizzled shared-memory stages of 64 reduction
 // elements:
 //
 //   grouped_cols_kernel   few rows per expert, bound by reading each touched expert's weights
@@ -28,9 +28,9 @@
 //
 // Sums: the tensor cores add into fp32 accumulators with truncation, an error that grows by about
 // 1.1e-9 (relative to the result) per reduction element (measured: 3.0e-6 at 2880, 6.3e-6 at
-// 5760, 1.9e-5 at 16384).  fp32 results therefore add reductions longer than 6144 elements up
-// from pieces of 6144 in the epilogue (round to nearest); bf16 results, whose rounding is 4e-3,
-// take one piece.
+// 5760, 1.9e-5 at 16384).  fp32 results therefore come from pieces of 640 elements, added in the
+// epilogue's registers with round to nearest (2.7e-7 ... 7e-7 in all); bf16 results, whose
+// rounding is 2e-3, take one piece.
 #pragma once
 
 #include "common.cuh"
@@ -42,7 +42,7 @@ namespace moe {
 
 constexpr int kGrMaxE = 256;
 constexpr int kGrBK = 64;           // reduction elements per stage (one 128-byte swizzle row)
-constexpr int kGrPieceStages = 96;  // stages per accumulator of an fp32 result (6144 elements)
+constexpr int kGrPieceStages = 10;  // stages per accumulator of an fp32 result (640 elements)
 
 MOE_DEVINL void tma_load_3d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
                             uint64_t* bar) {
@@ -108,6 +108,25 @@ MOE_DEVINL bool named_bar_and(int id, int nthreads, bool ok) {
       : "r"(id), "r"(nthreads), "r"((uint32_t)ok)
       : "memory");
   return r != 0;
+}
+// sum[i] += column taddr + i of this warp's 32 TMEM lanes (lane = thread), 16 columns at a time so
+// that the loaded values need few registers beside the sums.
+MOE_DEVINL void tmem_add32(uint32_t taddr, float (&sum)[32]) {
+#pragma unroll
+  for (int h = 0; h < 32; h += 16) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr + h)
+        : "memory");
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[h + i] += __uint_as_float(r[i]);
+  }
 }
 MOE_DEVINL float4 ld_cluster_f4(uint32_t cluster_addr) {
   float4 v;
@@ -180,16 +199,11 @@ struct GroupedArgs {
   uint32_t* status;
 };
 
-// Writes 4 fp32 values as OUT (float or bf16) to 4 consecutive columns.
+// Writes 4 fp32 values as fp32 or bf16 to 4 consecutive columns.
 template <bool F32>
-MOE_DEVINL void store4(void* out, size_t idx, float4 v, bool add) {
+MOE_DEVINL void store4(void* out, size_t idx, float4 v) {
   if constexpr (F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + idx);
-    if (add) {
-      const float4 o = *p;
-      v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
-    }
-    *p = v;
+    *reinterpret_cast<float4*>(static_cast<float*>(out) + idx) = v;
   } else {
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + idx) =
         make_uint2(cvt_bf16x2(v.x, v.y), cvt_bf16x2(v.z, v.w));
@@ -212,17 +226,18 @@ struct ColsCfg {
   static constexpr int kStages = ROWS == 32 ? 9 : 4;
   static constexpr int kAccBufs = 2;
   static constexpr int kTmemCols = kAccBufs * NM * ROWS;    // 64, 256, 512: powers of two
+  static constexpr int kEpiWarps = 4 * NM;                  // four per 128-column MMA
+  static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kPitch = kSplit ? 132 : 33;          // floats per staged row
-  static constexpr int kEpiBytes = kSplit ? ROWS * kPitch * 4 : 4 * 32 * kPitch * 4;
+  static constexpr int kEpiBytes = kSplit ? ROWS * kPitch * 4 : kEpiWarps * 16 * kPitch * 4;
   static constexpr int kSmem = 1024 + kStages * kStageBytes + 256 + kEpiBytes;
   static_assert(kStageBytes % 1024 == 0, "128-byte swizzle atoms");
   static_assert(kSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
 };
-constexpr int kColsThreads = 192;
 constexpr int kColsRowBox = 16;   // rows per TMA box
 
 template <int ROWS, int NM, bool TRANS, bool F32>
-__global__ void __launch_bounds__(kColsThreads, 1)
+__global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
     grouped_cols_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap wmap,
                         const __grid_constant__ CUtensorMap xmap, const int S) {
   using C = ColsCfg<ROWS, NM>;
@@ -256,7 +271,7 @@ __global__ void __launch_bounds__(kColsThreads, 1)
     }
     for (int b = 0; b < kBufs; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 128);
+      mbar_init(&acc_empty[b], 32 * C::kEpiWarps);
     }
     mbar_init(drain, 1);
     mbar_init(part_full, S);
@@ -278,7 +293,7 @@ __global__ void __launch_bounds__(kColsThreads, 1)
   const int NT = (a.Ncols + TW - 1) / TW;
   const int tiles = seg.base[a.E] * NT;
   const int nk_all = (a.Kred + kGrBK - 1) / kGrBK;
-  const int piece = !C::kSplit && F32 ? kGrPieceStages : nk_all;
+  const int piece = F32 ? kGrPieceStages : nk_all;
   const int group = C::kSplit ? (int)blockIdx.x / S : (int)blockIdx.x;
   const int groups = C::kSplit ? (int)gridDim.x / S : (int)gridDim.x;
   volatile int* abort_flag = &s_abort;
@@ -418,33 +433,65 @@ __global__ void __launch_bounds__(kColsThreads, 1)
     }
   } else {
     // ------------------------------ epilogue ------------------------------
-    // One TMEM lane (one weight column) per thread; the tile's rows are TMEM columns.
-    const int q = warp & 3;
+    // One TMEM lane (one weight column) per thread; the tile's rows are TMEM columns.  An fp32
+    // result's pieces are added in sum[][].
+    constexpr int kChunks = ROWS / 32;
+    const int q = warp & 3, m = (warp - 2) >> 2;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(32 * q) << 16) + m * ROWS;
     int unit = 0, ti = 0;
     bool ok = true;
     for (int t = group; ok && t < tiles; t += groups, ++ti) {
       const Tile w = tile_at(t);
       int k0, k1;
       k_range(t, k0, k1);
+      float sum[F32 ? kChunks : 1][32];
+      if constexpr (F32) {
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+        for (int p0 = k0; p0 < k1; p0 += piece, ++unit) {
+          const int buf = unit % kBufs;
+          ok = warp_wait(&acc_full[buf], (unit / kBufs) & 1u, abort_flag, a.status);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            if (32 * c < w.rows) tmem_add32(lane_base + buf * NM * ROWS + 32 * c, sum[c]);
+          tc_fence_before();
+          mbar_arrive(&acc_empty[buf]);
+        }
+      }
+      // rows 32 c .. 32 c + 31 of this thread's column
+      const int buf = unit % kBufs;
+      const bool any = !F32 && k1 > k0;   // one piece, still in tensor memory
+      auto chunk = [&](int c, float (&v)[32]) {
+        if constexpr (F32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = sum[c][i];
+        } else if (any) {
+          tmem_ld32(lane_base + buf * NM * ROWS + 32 * c, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+      };
+      if (ok && any) {
+        ok = warp_wait(&acc_full[buf], (unit / kBufs) & 1u, abort_flag, a.status);
+        tc_fence_after();
+      }
       if constexpr (C::kSplit) {
         // the previous tile's partial sums have been read by the whole cluster
-        ok = warp_wait_cluster(part_empty, (ti & 1) ^ 1u, abort_flag, a.status);
-        const int buf = unit % kBufs;
-        const bool any = k1 > k0;
-        if (ok && any) ok = warp_wait(&acc_full[buf], (unit / kBufs) & 1u, abort_flag, a.status);
+        if (ok) ok = warp_wait_cluster(part_empty, (ti & 1) ^ 1u, abort_flag, a.status);
         if (ok) {
-          tc_fence_after();
-          for (int r0 = 0; r0 < w.rows; r0 += 32) {
-            float v[32];
-            if (any) {
-              tmem_ld32(tmem_base + ((uint32_t)(32 * q) << 16) + buf * ROWS + r0, v);
-            } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] = 0.f;
+          for (int c = 0; c < kChunks; ++c)
+            if (32 * c < w.rows) {
+              float v[32];
+              chunk(c, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) epi[(32 * c + i) * C::kPitch + 32 * q + lane] = v[i];
             }
-#pragma unroll
-            for (int i = 0; i < 32; ++i) epi[(r0 + i) * C::kPitch + 32 * q + lane] = v[i];
-          }
           if (any) {
             tc_fence_before();
             mbar_arrive(&acc_empty[buf]);
@@ -467,44 +514,39 @@ __global__ void __launch_bounds__(kColsThreads, 1)
             const float4 o = ld_cluster_f4(mapa_shared(off, s));
             v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
           }
-          store4<F32>(a.out, (size_t)(w.row0 + r) * a.Ncols + w.n0 + col, v, false);
+          store4<F32>(a.out, (size_t)(w.row0 + r) * a.Ncols + w.n0 + col, v);
         }
         ok = named_bar_and(1, 128, ok);
         if (ok && et < S) mbar_arrive_cluster(mapa_shared(smem_u32(part_empty), et));
-      } else {
-        float* stage = epi + (warp - 2) * 32 * C::kPitch;
-        for (int p0 = k0; p0 < k1; p0 += piece, ++unit) {
-          const int buf = unit % kBufs;
-          if (!warp_wait(&acc_full[buf], (unit / kBufs) & 1u, abort_flag, a.status)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t tb = tmem_base + ((uint32_t)(32 * q) << 16) + buf * NM * ROWS;
-#pragma unroll 1
-          for (int m = 0; m < NM; ++m) {
-            const int col0 = w.n0 + 128 * m + 32 * q;
-            if (col0 >= a.Ncols) continue;  // warp-uniform
-            for (int r0 = 0; r0 < w.rows; r0 += 32) {
-              float v[32];
-              tmem_ld32(tb + m * ROWS + r0, v);
+      } else if (ok) {
+        float* stage = epi + (warp - 2) * 16 * C::kPitch;
+        const int col0 = w.n0 + 128 * m + 32 * q;
 #pragma unroll
-              for (int i = 0; i < 32; ++i) stage[i * C::kPitch + lane] = v[i];
-              __syncwarp();
-              // 8 lanes cover the 32 columns of a row
+        for (int c = 0; c < kChunks; ++c) {
+          if (32 * c >= w.rows || col0 >= a.Ncols) continue;  // warp-uniform
+          float v[32];
+          chunk(c, v);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const int r = 4 * i + (lane >> 3), cc = 4 * (lane & 7);
-                const float* sp = stage + r * C::kPitch + cc;
-                if (r0 + r < w.rows && col0 + cc < a.Ncols)
-                  store4<F32>(a.out, (size_t)(w.row0 + r0 + r) * a.Ncols + col0 + cc,
-                              make_float4(sp[0], sp[1], sp[2], sp[3]), p0 > k0);
-              }
-              __syncwarp();
+          for (int h = 0; h < 2; ++h) {   // 16 rows at a time
+#pragma unroll
+            for (int i = 0; i < 16; ++i) stage[i * C::kPitch + lane] = v[16 * h + i];
+            __syncwarp();
+            // 8 lanes cover the 32 columns of a row
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 4 * i + (lane >> 3), row = 32 * c + 16 * h + r, cc = 4 * (lane & 7);
+              const float* sp = stage + r * C::kPitch + cc;
+              if (row < w.rows && col0 + cc < a.Ncols)
+                store4<F32>(a.out, (size_t)(w.row0 + row) * a.Ncols + col0 + cc,
+                            make_float4(sp[0], sp[1], sp[2], sp[3]));
             }
+            __syncwarp();
           }
+        }
+        if (any) {
           tc_fence_before();
           mbar_arrive(&acc_empty[buf]);
+          ++unit;
         }
       }
     }
@@ -524,69 +566,100 @@ constexpr int kPairStages = 6;
 constexpr int kPairHalf = 128;                                 // rows and columns staged per CTA
 constexpr int kPairABytes = kPairHalf * kGrBK * 2;             // 16 KB
 constexpr int kPairStageBytes = 2 * kPairABytes;               // 32 KB per CTA
-constexpr int kPairEpiPitch = 36;                              // 32-bit words per staged row
-constexpr int kPairEpiBytes = 4 * 32 * kPairEpiPitch * 4;
+constexpr int kPairEpiWarps = 8;                               // two per TMEM lane quarter
+constexpr int kPairEpiPitch = 20;                              // 32-bit words per staged row of 16
+constexpr int kPairEpiBytes = kPairEpiWarps * 32 * kPairEpiPitch * 4;
 constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 256 + kPairEpiBytes;
-constexpr int kPairThreads = 192;
-constexpr int kWgradThreads = 224;                             // + the warp that masks ragged ends
+constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
+constexpr int kWgradThreads = kPairThreads + 32;               // + the warp that masks ragged ends
 static_assert(kPairSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
 
-// One warp's 32 rows x 256 accumulator columns to `out` (row stride ld, this warp's first row and
-// the tile's first column already in row0 / n0), through a shared-memory transpose so that eight
-// lanes write 128 contiguous bytes of one row.  rows_ok: valid rows of the 32 (may be <= 0).
-// zero: write zeros instead of the accumulators.  add: fp32 results add to what is there.
+// One warp's 32 rows x 64 bytes (16 words w per lane, lane = row) to columns col0 .. of `out` (row
+// stride ld, first row row0), through shared memory so that four lanes write 64 contiguous bytes
+// of a row.  rows_ok: valid rows of the 32.
 template <bool F32>
-MOE_DEVINL void pair_store(uint32_t taddr, uint32_t* stage, int lane, void* out, size_t row0,
-                           int rows_ok, int n0, int ld, bool zero, bool add) {
-  constexpr int kCols = F32 ? 32 : 64;   // columns per 128 bytes
-#pragma unroll 1
-  for (int c = 0; c < 256; c += kCols) {
-    if (n0 + c >= ld) break;             // warp-uniform
-    uint32_t w[32];
-    if (zero) {
+MOE_DEVINL void pair_store(const uint32_t* w, uint32_t* stage, int lane, void* out, size_t row0,
+                           int rows_ok, int col0, int ld) {
+  uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPairEpiPitch);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = 0u;
-    } else if constexpr (F32) {
-      float v[32];
-      tmem_ld32(taddr + c, v);
+  for (int i = 0; i < 4; ++i)
+    mine[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  __syncwarp();
+  const int col = col0 + (lane & 3) * (F32 ? 4 : 8);
 #pragma unroll
-      for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(v[i]);
-    } else {
-      float v[32];
-      tmem_ld32(taddr + c, v);
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kPairEpiPitch + 4 * (lane & 3));
+    if (r < rows_ok && col < ld)
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + ((row0 + r) * ld + col) * (F32 ? 4 : 2)) = v;
+  }
+  __syncwarp();
+}
+
+// The epilogue of one tile for one warp: 32 rows (TMEM lanes of its quarter) x 128 columns, from
+// `pieces` accumulators in turn.  taddr: this warp's lanes and first column in buffer 0.  unit: the
+// accumulators handed over so far.  rows_ok <= 0: nothing to write, the hand-over only.
+// pieces = 0 writes zeros.  Returns false when a wait gave up.
+template <bool F32>
+MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* acc_full,
+                              uint64_t* acc_empty, uint32_t* stage, int lane, void* out,
+                              size_t row0, int rows_ok, int col0, int ld, volatile int* abort_flag,
+                              uint32_t* status) {
+  const bool mine = rows_ok > 0 && col0 < ld;   // warp-uniform
+  if constexpr (F32) {
+    float sum[4][32];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
-      tmem_ld32(taddr + c + 32, v);
+    for (int c = 0; c < 4; ++c)
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[16 + i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+      for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+    for (int p = 0; p < pieces; ++p, ++unit) {
+      const int buf = unit & 1;
+      if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, status)) return false;
+      tc_fence_after();
+      if (mine) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_add32(taddr + buf * 256 + 32 * c, sum[c]);
+      }
+      tc_fence_before();
+      mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
     }
-    uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPairEpiPitch);
+    if (!mine) return true;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      mine[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    __syncwarp();
-    const int cc = n0 + c + (lane & 7) * (kCols / 8);
+    for (int c = 0; c < 8; ++c) {
+      uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = 4 * i + (lane >> 3);
-      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kPairEpiPitch + 4 * (lane & 7));
-      if (r < rows_ok && cc < ld) {
-        if constexpr (F32) {
-          float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + (row0 + r) * ld + cc);
-          float4 f = make_float4(__uint_as_float(v.x), __uint_as_float(v.y),
-                                 __uint_as_float(v.z), __uint_as_float(v.w));
-          if (add) {
-            const float4 o = *p;
-            f = make_float4(f.x + o.x, f.y + o.y, f.z + o.z, f.w + o.w);
-          }
-          *p = f;
+      for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(sum[c / 2][16 * (c % 2) + i]);
+      pair_store<true>(w, stage, lane, out, row0, rows_ok, col0 + 16 * c, ld);
+    }
+  } else {
+    const int buf = unit & 1;
+    if (pieces > 0) {
+      if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, status)) return false;
+      tc_fence_after();
+    }
+    if (mine) {
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+        if (pieces > 0) {
+          float v[32];
+          tmem_ld32(taddr + buf * 256 + 32 * c, v);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
         } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + (row0 + r) * ld + cc) = v;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = 0u;
         }
+        pair_store<false>(w, stage, lane, out, row0, rows_ok, col0 + 32 * c, ld);
       }
     }
-    __syncwarp();
+    if (pieces > 0) {
+      tc_fence_before();
+      mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+      ++unit;
+    }
   }
+  return true;
 }
 
 // Many rows per expert.  Tile: 256 rows of one expert x 256 columns; each CTA of the pair stages
@@ -624,7 +697,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 2 * 128);
+      mbar_init(&acc_empty[b], 2 * 32 * kPairEpiWarps);
     }
     mbar_init(drain, 1);
     s_abort = 0;
@@ -756,26 +829,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
   } else {
     // ------------------------------ epilogue (both CTAs) ------------------------------
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + 128 * half;
     uint32_t* stage = epi + (warp - 2) * 32 * kPairEpiPitch;
+    const int pieces = (nk + piece - 1) / piece;
+    const int r0 = rank * kPairHalf + 32 * q;   // this warp's first row of a tile
     int unit = 0;
-    bool ok = true;
-    for (int t = pair; ok && t < tiles; t += npairs) {
+    for (int t = pair; t < tiles; t += npairs) {
       const Tile w = tile_at(t);
-      for (int p0 = 0; p0 < nk; p0 += piece, ++unit) {
-        const int buf = unit & 1;
-        if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, a.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const int r0 = rank * kPairHalf + 32 * q;   // this warp's first row of the tile
-        if (r0 < w.rows)
-          pair_store<F32>(tmem_base + ((uint32_t)(32 * q) << 16) + buf * 256, stage, lane, a.out,
-                          (size_t)w.row0 + r0, w.rows - r0, w.n0, a.Ncols, false, p0 > 0);
-        tc_fence_before();
-        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
-      }
+      if (!pair_epilogue<F32>(taddr, pieces, unit, acc_full, acc_empty, stage, lane, a.out,
+                              (size_t)w.row0 + r0, w.rows - r0, w.n0 + 128 * half, a.Ncols,
+                              abort_flag, a.status))
+        break;
     }
   }
 
@@ -829,7 +894,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 2 * 128);
+      mbar_init(&acc_empty[b], 2 * 32 * kPairEpiWarps);
     }
     mbar_init(drain, 1);
     s_abort = 0;
@@ -936,8 +1001,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             tc_fence_after();
             const uint64_t soff = (uint64_t)((slot * kPairStageBytes) >> 4);
             const int steps = min(kGrBK / 16, (cnt - r + 15) / 16);
-            for (int k16 = 0; k16 < steps; ++k16)
-              tc_mma_bf16_2sm(d, adesc0 + soff + ((k16 * 2048) >> 4),
+#pragma unroll
+            for (int k16 = 0; k16 < kGrBK / 16; ++k16)
+              if (k16 < steps) tc_mma_bf16_2sm(d, adesc0 + soff + ((k16 * 2048) >> 4),
                               bdesc0 + soff + ((k16 * 2048) >> 4), idesc, r != p0 || k16 != 0);
             const uint32_t e_local = smem_u32(&empty[slot]);
             tc_commit_2sm(e_local);
@@ -956,7 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         if (!mbar_wait_bounded(drain, 0, kWaitLimitNs)) atomicOr(a.status, kStatusTimeout);
       }
     }
-  } else if (warp == 6) {
+  } else if (warp == 2 + kPairEpiWarps) {
     // ------------------------------ masking of ragged ends (both CTAs) ------------------------
     uint32_t it = 0, ragged_ph = 0;
     for (int t = pair; t < tiles; t += npairs) {
@@ -986,33 +1052,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     }
   } else {
     // ------------------------------ epilogue (both CTAs) ------------------------------
-    const int q = warp & 3;
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + 128 * half;
     uint32_t* stage = epi + (warp - 2) * 32 * kPairEpiPitch;
     int unit = 0;
-    bool ok = true;
-    for (int t = pair; ok && t < tiles; t += npairs) {
+    for (int t = pair; t < tiles; t += npairs) {
       const int e = t / per, l = t - e * per;
-      const int m0 = l / NT * 256 + rank * kPairHalf + 32 * q, n0 = l % NT * 256;
+      const int m0 = l / NT * 256 + rank * kPairHalf + 32 * q, n0 = l % NT * 256 + 128 * half;
       const int cnt = seg.cnt[e];
-      const int piece = F32 ? kGrPieceStages * kGrBK : max(cnt, 1);
-      const size_t row0 = (size_t)e * a.M + m0;
-      if (cnt == 0) {
-        if (m0 < a.M) pair_store<F32>(0, stage, lane, a.out, row0, a.M - m0, n0, a.Ncols, true, false);
-        continue;
-      }
-      for (int p0 = 0; p0 < cnt; p0 += piece, ++unit) {
-        const int buf = unit & 1;
-        if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, a.status)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (m0 < a.M)
-          pair_store<F32>(tmem_base + ((uint32_t)(32 * q) << 16) + buf * 256, stage, lane, a.out,
-                          row0, a.M - m0, n0, a.Ncols, false, p0 > 0);
-        tc_fence_before();
-        mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
-      }
+      const int pieces = F32 ? (cnt + kGrPieceStages * kGrBK - 1) / (kGrPieceStages * kGrBK) : cnt > 0;
+      if (!pair_epilogue<F32>(taddr, pieces, unit, acc_full, acc_empty, stage, lane, a.out,
+                              (size_t)e * a.M + m0, a.M - m0, n0, a.Ncols, abort_flag, a.status))
+        break;
     }
   }
 

@@ -93,7 +93,7 @@ bool query_clusters(int num_sms, int* out) {
     const int size = 2 << i;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms / size * size);
-    cfg.blockDim = dim3(kColsThreads);
+    cfg.blockDim = dim3(ColsCfg<kColsSmallRows, 1>::kThreads);
     cfg.dynamicSmemBytes = ColsCfg<kColsSmallRows, 1>::kSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -152,7 +152,7 @@ cudaError_t launch_cols(const moe_ctx* c, int split, const GroupedArgs& a, const
   auto kernel = grouped_cols_kernel<ROWS, NM, TRANS, F32>;
   const size_t smem = ColsCfg<ROWS, NM>::kSmem;
   const int clusters = split == 1 ? c->num_sms : c->max_clusters[split / 4];  // 2, 4, 8 -> 0, 1, 2
-  return launch_pdl_cluster(kernel, dim3(clusters * split), dim3(kColsThreads), smem, split, st, a,
+  return launch_pdl_cluster(kernel, dim3(clusters * split), dim3(ColsCfg<ROWS, NM>::kThreads), smem, split, st, a,
                             wmap, xmap, split);
 }
 
