@@ -74,7 +74,6 @@ template <bool TRANS, bool F32>
 bool set_grouped_attrs() {
   return smem_attr(grouped_cols_kernel<kColsSmallRows, 1, TRANS, F32>,
                    ColsCfg<kColsSmallRows, 1>::kSmem) &&
-         smem_attr(grouped_cols_kernel<kColsRows, 1, TRANS, F32>, ColsCfg<kColsRows, 1>::kSmem) &&
          smem_attr(grouped_cols_kernel<kColsRows, 2, TRANS, F32>, ColsCfg<kColsRows, 2>::kSmem) &&
          smem_attr(grouped_rows_kernel<TRANS, F32>, kPairSmem);
 }
@@ -86,10 +85,10 @@ bool set_rows_smem_attrs() {
          smem_attr(grouped_wgrad_kernel<true>, kPairSmem);
 }
 
-// Clusters of 2, 4 and 8 CTAs of the few-row kernel (one CTA per SM) that fit the GPU at once: a
+// Clusters of 2 and 4 CTAs of the few-row kernel (one CTA per SM) that fit the GPU at once: a
 // cluster lies inside one GPC, whose SM count need not be a multiple of its size.
 bool query_clusters(int num_sms, int* out) {
-  for (int i = 0; i < 3; ++i) {
+  for (int i = 0; i < 2; ++i) {
     const int size = 2 << i;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms / size * size);
@@ -111,39 +110,61 @@ bool query_clusters(int num_sms, int* out) {
 }
 
 // Which kernel multiplies a call's rows, from sizes the host knows (the segments stay on the
-// device).
+// device): the one with the smallest estimate.
 struct GroupedPlan {
-  enum Kind { kColsSmall, kCols, kColsWide, kRows } kind;
+  enum Kind { kColsSmall, kColsWide, kRows } kind;
   int split;    // CTAs per cluster that share a tile's reduction
 };
 
+// Estimate in us of `tiles` tiles on `slots` CTAs (or pairs) at a time, `stages` stages each: a
+// stage takes at least `stage_us`, or as long as HBM needs for the weight bytes that all slots
+// load in it; `tile_us` more per tile.
+double grouped_us(long long tiles, int slots, double stages, double stage_us, double hbm_bytes,
+                  double tile_us) {
+  const double us_per_byte = 1.0 / 6.5e6;
+  const long long full = tiles / slots, rem = tiles % slots;
+  auto round = [&](double n) {
+    return stages * std::max(stage_us, n * hbm_bytes * us_per_byte) + tile_us;
+  };
+  return full * round(slots) + (rem ? round((double)rem) : 0.0);
+}
+
+// The constants are fitted to 176 measured calls (1..128 experts of 2..640 rows, four weight
+// shapes; bf16, graph replay): the choice costs 0.2 % over the best kernel of each, 13 % at worst.
+// Some of them, us as 128-column tiles / split in two / in four / 256-column tiles / pairs:
+//   1 expert of 4 rows, 2880 x 2880          18.0 / 11.7 / 8.8 / 22.7 / 19.0
+//   8 experts of 4 rows, 2880 x 2880         36.7 / 30.5 / 31.1 / 25.6 / 35.6
+//   8 experts of 4 rows, 2880 x 5760         52.7 / 46.6 / 50.8 / 54.8 / 52.3
+//   32 experts of 128 rows, 2880 x 2880      256 columns 97, pairs 122
+//   32 experts of 192 rows, 2880 x 2880      256 columns 195, pairs 123
 GroupedPlan plan_grouped(const moe_ctx* c, int R, int Kred, int Ncols) {
   const int nk = (Kred + kGrBK - 1) / kGrBK;
-  const long long mean = ((long long)R + c->E - 1) / c->E;
-  const long long busy = std::min(R, c->E);      // experts that can hold rows
-  auto tiles = [&](int rows, int cols) {
-    return busy * ((mean + rows - 1) / rows) * ((Ncols + cols - 1) / cols);
+  const int busy = std::min(R, c->E);                // experts that can hold rows
+  const int mean = (R + busy - 1) / busy;
+  auto chunks = [&](int rows) { return (long long)(mean + rows - 1) / rows; };
+  auto blocks = [&](int cols) { return (long long)(Ncols + cols - 1) / cols; };
+  GroupedPlan best{GroupedPlan::kRows, 1};
+  double us = grouped_us(busy * chunks(256) * blocks(256), c->num_sms / 2, nk, 0.36, 0.0, 0.8);
+  auto consider = [&](GroupedPlan p, double t) {
+    if (t < us) {
+      best = p;
+      us = t;
+    }
   };
-  auto split_for = [&](long long n) {            // enough CTAs for about four waves of tiles
-    int s = 1;
-    while (s < 8 && n * s < 4ll * c->num_sms && nk >= 8 * s) s *= 2;
-    return s;
-  };
-  GroupedPlan p;
-  if (mean <= kColsSmallRows / 2) {
-    p.kind = GroupedPlan::kColsSmall;
-    p.split = split_for(tiles(kColsSmallRows, 128));
-  } else if (mean > 160 && tiles(256, 256) >= c->num_sms / 2) {
-    p.kind = GroupedPlan::kRows;
-    p.split = 1;
-  } else if (tiles(kColsRows, 256) >= 2ll * c->num_sms) {
-    p.kind = GroupedPlan::kColsWide;
-    p.split = 1;
-  } else {
-    p.kind = GroupedPlan::kCols;
-    p.split = split_for(tiles(kColsRows, 128));
-  }
-  return p;
+  // a weight block is read from HBM once for all chunks of its expert
+  consider({GroupedPlan::kColsWide, 1},
+           grouped_us(busy * chunks(kColsRows) * blocks(256), c->num_sms, nk,
+                      0.40 + 0.15 * std::min(mean, kColsRows) / kColsRows,
+                      32768.0 / chunks(kColsRows), 0.1));
+  if (mean <= 4 * kColsSmallRows)
+    for (int s = 1; s <= 4; s *= 2) {
+      const int slots = s == 1 ? c->num_sms : c->max_clusters[s / 4];
+      consider({GroupedPlan::kColsSmall, s},
+               grouped_us(busy * chunks(kColsSmallRows) * blocks(128), slots, (double)nk / s, 0.34,
+                          s * 16384.0 / chunks(kColsSmallRows),
+                          0.3 + 0.03 * std::min(mean, kColsSmallRows) + (s > 1 ? 0.4 : 0.0)));
+    }
+  return best;
 }
 
 template <int ROWS, int NM, bool TRANS, bool F32>
@@ -151,7 +172,7 @@ cudaError_t launch_cols(const moe_ctx* c, int split, const GroupedArgs& a, const
                         const CUtensorMap& xmap, cudaStream_t st) {
   auto kernel = grouped_cols_kernel<ROWS, NM, TRANS, F32>;
   const size_t smem = ColsCfg<ROWS, NM>::kSmem;
-  const int clusters = split == 1 ? c->num_sms : c->max_clusters[split / 4];  // 2, 4, 8 -> 0, 1, 2
+  const int clusters = split == 1 ? c->num_sms : c->max_clusters[split / 4];  // 2, 4 -> 0, 1
   return launch_pdl_cluster(kernel, dim3(clusters * split), dim3(ColsCfg<ROWS, NM>::kThreads), smem, split, st, a,
                             wmap, xmap, split);
 }
@@ -160,18 +181,18 @@ template <bool TRANS, bool F32>
 moe_status run_grouped(moe_ctx* c, const GroupedArgs& a, const void* W, const void* x, int K, int N,
                        cudaStream_t st) {
   const GroupedPlan p = plan_grouped(c, a.R, a.Kred, a.Ncols);
-  const bool rows = p.kind == GroupedPlan::kRows;
+  const uint32_t box = p.kind == GroupedPlan::kRows       ? kPairHalf
+                       : p.kind == GroupedPlan::kColsWide ? ColsCfg<kColsRows, 2>::kRowBox
+                                                          : ColsCfg<kColsSmallRows, 1>::kRowBox;
   CUtensorMap wmap, xmap;
   // transposed: boxes of 128 weight rows (columns of the result) x 64; else 64 x 64
   if (!encode_planes(&wmap, W, c->E, K, N, TRANS ? 128 : kGrBK) ||
-      !encode_rows(&xmap, x, a.R, a.Kred, rows ? kPairHalf : kColsRowBox))
+      !encode_rows(&xmap, x, a.R, a.Kred, box))
     return MOE_ERR_CUDA;
   return launch(c, -1, st, [&] {
     switch (p.kind) {
       case GroupedPlan::kColsSmall:
         return launch_cols<kColsSmallRows, 1, TRANS, F32>(c, p.split, a, wmap, xmap, st);
-      case GroupedPlan::kCols:
-        return launch_cols<kColsRows, 1, TRANS, F32>(c, p.split, a, wmap, xmap, st);
       case GroupedPlan::kColsWide:
         return launch_cols<kColsRows, 2, TRANS, F32>(c, p.split, a, wmap, xmap, st);
       default:
