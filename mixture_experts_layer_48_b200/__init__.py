@@ -116,6 +116,12 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape=None) -> i
     return t.data_ptr()
 
 
+# The current stream's handle; torch's own short way to it where it has one (a tenth of a
+# microsecond instead of three for a Stream object).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _stream(stream) -> int:
     s = torch.cuda.current_stream() if stream is None else stream
     return s.cuda_stream
@@ -141,7 +147,7 @@ class Moe:
         _check(moe_create(E, H, I, k, ctypes.byref(h)), "moe_create")
         self._h = h
         self._ws = None
-        self._device = torch.device("cuda", torch.cuda.current_device())
+        self._device_index = torch.cuda.current_device()
 
     # -- lifetime --------------------------------------------------------------------
     def close(self):
@@ -284,75 +290,98 @@ class Moe:
         return out
 
     # -- training and the block around the layer (include/moe.h) ------------------------
-    # Result tensors and workspaces that a call makes belong to the stream it runs on.
-    def _on(self, stream, *tensors):
-        """Context of one call: its tensors must be on the handle's device, which becomes current,
-        and what it allocates belongs to the stream it enqueues on."""
-        for t in tensors:
-            if t is not None and t.device != self._device:
-                raise ValueError(f"tensors must be on {self._device}, got one on {t.device}")
-        return torch.cuda.stream(torch.cuda.current_stream(self._device) if stream is None else stream)
+    # A call with stream= runs as one inside torch.cuda.stream(stream): what it allocates (results,
+    # workspaces) belongs to the stream it enqueues on.  Tensors must be on the handle's device,
+    # which must be the current one.
+    def _arg(self, t, dtype, name: str, shape) -> int:
+        """Address of an argument after its checks; 0 for None."""
+        if t is None:
+            return 0
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+        if t.get_device() != self._device_index:
+            raise ValueError(f"{name} must be on cuda:{self._device_index}, got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return t.data_ptr()
+
+    def _current(self) -> int:
+        return _raw_stream(self._device_index)
 
     def grouped_matmul(self, x_rows, W, offsets, transpose: bool = False, out=None,
                        out_dtype=torch.bfloat16, stream=None) -> torch.Tensor:
         """x_rows[r] @ W[e] (transpose: @ W[e].T) for the rows offsets[e] <= r < offsets[e+1] of
         every expert e.  W [E, K, N]; offsets [E + 1] int32.  `out` (bf16 or fp32) keeps its rows
         outside the segments; without it they are not set."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.grouped_matmul(x_rows, W, offsets, transpose, out, out_dtype)
         if W.dim() != 3 or x_rows.dim() != 2:
             raise ValueError("x_rows must be [R, K] (transpose: [R, N]) and W [E, K, N]")
         E, K, N = W.shape
         ins, outs = (N, K) if transpose else (K, N)
-        R = x_rows.shape[0]
-        with self._on(stream, x_rows, W, offsets, out):
-            if out is None:
-                out = torch.empty((R, outs), dtype=out_dtype, device=x_rows.device)
-            st = moe_grouped_matmul(
-                self._h, R, K, N, int(transpose), _ptr(offsets, torch.int32, "offsets", (self.E + 1,)),
-                _ptr(x_rows, torch.bfloat16, "x_rows", (R, ins)),
-                _ptr(W, torch.bfloat16, "W", (self.E, K, N)), _ptr(out, out.dtype, "out", (R, outs)),
-                _dtype(out, "out"), _stream(None))
+        R, bf16 = x_rows.shape[0], torch.bfloat16
+        px = self._arg(x_rows, bf16, "x_rows", (R, ins))
+        pw = self._arg(W, bf16, "W", (self.E, K, N))
+        po = self._arg(offsets, torch.int32, "offsets", (self.E + 1,))
+        kind = _dtype(out_dtype if out is None else out, "out")
+        if out is None:
+            out = x_rows.new_empty((R, outs), dtype=out_dtype)
+        st = moe_grouped_matmul(self._h, R, K, N, int(transpose), po, px, pw,
+                                self._arg(out, out.dtype, "out", (R, outs)), kind, self._current())
         _check(st, "moe_grouped_matmul")
         return out
 
     def grouped_wgrad(self, x_rows, dy_rows, offsets, out=None, out_dtype=torch.bfloat16,
                       stream=None) -> torch.Tensor:
         """dW [E, K, N]: dW[e] = x_rows[rows of e].T @ dy_rows[rows of e], zeros without rows."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.grouped_wgrad(x_rows, dy_rows, offsets, out, out_dtype)
         if x_rows.dim() != 2 or dy_rows.dim() != 2:
             raise ValueError("x_rows must be [R, K] and dy_rows [R, N]")
         (R, K), N = x_rows.shape, dy_rows.shape[1]
-        with self._on(stream, x_rows, dy_rows, offsets, out):
-            if out is None:
-                out = torch.empty((self.E, K, N), dtype=out_dtype, device=x_rows.device)
-            st = moe_grouped_wgrad(
-                self._h, R, K, N, _ptr(offsets, torch.int32, "offsets", (self.E + 1,)),
-                _ptr(x_rows, torch.bfloat16, "x_rows", (R, K)),
-                _ptr(dy_rows, torch.bfloat16, "dy_rows", (R, N)),
-                _ptr(out, out.dtype, "out", (self.E, K, N)), _dtype(out, "out"), _stream(None))
+        px = self._arg(x_rows, torch.bfloat16, "x_rows", (R, K))
+        pdy = self._arg(dy_rows, torch.bfloat16, "dy_rows", (R, N))
+        po = self._arg(offsets, torch.int32, "offsets", (self.E + 1,))
+        kind = _dtype(out_dtype if out is None else out, "out")
+        if out is None:
+            out = x_rows.new_empty((self.E, K, N), dtype=out_dtype)
+        st = moe_grouped_wgrad(self._h, R, K, N, po, px, pdy,
+                               self._arg(out, out.dtype, "out", (self.E, K, N)), kind,
+                               self._current())
         _check(st, "moe_grouped_wgrad")
         return out
 
     def swiglu(self, gu, row_w=None, out=None, stream=None) -> torch.Tensor:
         """row_w[r] * silu(gu[r, :I]) * gu[r, I:] -> [R, I] bf16 (row_w None: 1)."""
-        R = gu.shape[0]
-        with self._on(stream, gu, row_w, out):
-            if out is None:
-                out = torch.empty((R, self.I), dtype=torch.bfloat16, device=gu.device)
-            st = moe_swiglu(self._h, R, _ptr(gu, torch.bfloat16, "gu", (R, 2 * self.I)),
-                            _ptr(row_w, torch.float32, "row_w", (R,)),
-                            _ptr(out, torch.bfloat16, "out", (R, self.I)), _stream(None))
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.swiglu(gu, row_w, out)
+        R, I, bf16 = gu.shape[0], self.I, torch.bfloat16
+        pg = self._arg(gu, bf16, "gu", (R, 2 * I))
+        pw = self._arg(row_w, torch.float32, "row_w", (R,))
+        if out is None:
+            out = gu.new_empty((R, I))
+        st = moe_swiglu(self._h, R, pg, pw, self._arg(out, bf16, "out", (R, I)), self._current())
         _check(st, "moe_swiglu")
         return out
 
     def swiglu_backward(self, dh, gu, row_w=None, stream=None) -> tuple:
         """(dgu [R, 2I] bf16, drow_w [R] fp32, or None without row_w) from dh [R, I]."""
-        R = gu.shape[0]
-        with self._on(stream, dh, gu, row_w):
-            dgu = torch.empty((R, 2 * self.I), dtype=torch.bfloat16, device=gu.device)
-            dw = None if row_w is None else torch.empty((R,), dtype=torch.float32, device=gu.device)
-            st = moe_swiglu_backward(self._h, R, _ptr(dh, torch.bfloat16, "dh", (R, self.I)),
-                                     _ptr(gu, torch.bfloat16, "gu", (R, 2 * self.I)),
-                                     _ptr(row_w, torch.float32, "row_w", (R,)), dgu.data_ptr(),
-                                     _ptr(dw, torch.float32, "drow_w"), _stream(None))
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.swiglu_backward(dh, gu, row_w)
+        R, I, bf16 = gu.shape[0], self.I, torch.bfloat16
+        pd = self._arg(dh, bf16, "dh", (R, I))
+        pg = self._arg(gu, bf16, "gu", (R, 2 * I))
+        pw = self._arg(row_w, torch.float32, "row_w", (R,))
+        dgu = gu.new_empty((R, 2 * I))
+        dw = None if row_w is None else row_w.new_empty((R,))
+        st = moe_swiglu_backward(self._h, R, pd, pg, pw, dgu.data_ptr(),
+                                 0 if dw is None else dw.data_ptr(), self._current())
         _check(st, "moe_swiglu_backward")
         return dgu, dw
 
@@ -362,26 +391,28 @@ class Moe:
         block in one pass.  Returns resid (the new residual: resid + scale * gate * norm(y), in
         resid's type; resid itself without y), x (its norm, bf16; None without w_next) and
         rstd_post, rstd_next for the backward pass."""
-        T, H = resid.shape[0], self.H
-        dev = resid.device
-        with self._on(stream, resid, y, w_post, gate, w_next, resid_out):
-            if resid_out is None and y is not None:
-                resid_out = torch.empty_like(resid)
-            x = rp = rn = None
-            if w_post is not None:
-                rp = torch.empty((T,), dtype=torch.float32, device=dev)
-            if w_next is not None:
-                x = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-                rn = torch.empty((T,), dtype=torch.float32, device=dev)
-            st = moe_block_norm(
-                self._h, T, _dtype(resid, "resid"), MOE_F32 if y is None else _dtype(y, "y"),
-                _ptr(resid, resid.dtype, "resid", (T, H)),
-                _ptr(y, None if y is None else y.dtype, "y", (T, H)),
-                _ptr(w_post, torch.float32, "w_post", (H,)), _ptr(gate, torch.float32, "gate", (H,)),
-                scale, _ptr(w_next, torch.float32, "w_next", (H,)), eps,
-                _ptr(resid_out, resid.dtype, "resid_out", (T, H)), _ptr(x, torch.bfloat16, "x"),
-                _ptr(rp, torch.float32, "rstd_post"), _ptr(rn, torch.float32, "rstd_next"),
-                _stream(None))
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.block_norm(resid, y, w_post, gate, scale, w_next, eps, resid_out)
+        T, H, f32 = resid.shape[0], self.H, torch.float32
+        pr = self._arg(resid, resid.dtype, "resid", (T, H))
+        py = self._arg(y, None if y is None else y.dtype, "y", (T, H))
+        pp = self._arg(w_post, f32, "w_post", (H,))
+        pg = self._arg(gate, f32, "gate", (H,))
+        pn = self._arg(w_next, f32, "w_next", (H,))
+        rt, yt = _dtype(resid, "resid"), MOE_F32 if y is None else _dtype(y, "y")
+        if resid_out is None and y is not None:
+            resid_out = resid.new_empty((T, H))
+        x = rp = rn = None
+        if w_post is not None:
+            rp = w_post.new_empty((T,))
+        if w_next is not None:
+            x = resid.new_empty((T, H), dtype=torch.bfloat16)
+            rn = w_next.new_empty((T,))
+        st = moe_block_norm(
+            self._h, T, rt, yt, pr, py, pp, pg, scale, pn, eps,
+            self._arg(resid_out, resid.dtype, "resid_out", (T, H)), 0 if x is None else x.data_ptr(),
+            0 if rp is None else rp.data_ptr(), 0 if rn is None else rn.data_ptr(), self._current())
         _check(st, "moe_block_norm")
         return dict(resid=resid if y is None else resid_out, x=x, rstd_post=rp, rstd_next=rn)
 
@@ -396,29 +427,37 @@ class Moe:
         where nothing flows), resid, rstd_post and rstd_next its results.  Returns dresid (the
         gradient of the old residual), dy (None for the norm before a first block: `block` False,
         the default without y), dw_post, dgate and dw_next (None where the vector is)."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.block_norm_backward(dresid, dx, resid, y, rstd_post, rstd_next, w_post,
+                                                gate, scale, w_next, block, dy_dtype, None, workspace)
         like = dresid if dresid is not None else resid
-        (T, H), dev = like.shape, like.device
+        T, H, f32, rtype = like.shape[0], self.H, torch.float32, like.dtype
         has_block = (y is not None) if block is None else block
-        with self._on(stream, dresid, dx, resid, y, rstd_post, rstd_next, w_post, gate, w_next, workspace):
-            vec = lambda v: None if v is None else torch.empty((H,), dtype=torch.float32, device=dev)  # noqa: E731
-            out = dict(dresid=torch.empty((T, H), dtype=like.dtype, device=dev),
-                       dy=torch.empty((T, H), dtype=dy_dtype, device=dev) if has_block else None,
-                       dw_post=vec(w_post), dgate=vec(gate), dw_next=vec(w_next))
-            ws = workspace
-            if ws is None and not (w_post is None and gate is None and w_next is None):
-                ws = torch.empty((self.block_norm_workspace_bytes(T),), dtype=torch.uint8, device=dev)
-            f32 = torch.float32
-            st = moe_block_norm_backward(
-                self._h, T, _dtype(like, "dresid"), MOE_F32 if y is None else _dtype(y, "y"),
-                _dtype(dy_dtype, "dy_dtype"), _ptr(dresid, like.dtype, "dresid", (T, H)),
-                _ptr(dx, torch.bfloat16, "dx", (T, H)), _ptr(resid, like.dtype, "resid", (T, H)),
-                _ptr(y, None if y is None else y.dtype, "y", (T, H)),
-                _ptr(rstd_post, f32, "rstd_post", (T,)), _ptr(rstd_next, f32, "rstd_next", (T,)),
-                _ptr(w_post, f32, "w_post", (H,)), _ptr(gate, f32, "gate", (H,)), scale,
-                _ptr(w_next, f32, "w_next", (H,)), out["dresid"].data_ptr(),
-                _ptr(out["dy"], dy_dtype, "dy"), _ptr(out["dw_post"], f32, "dw_post"),
-                _ptr(out["dgate"], f32, "dgate"), _ptr(out["dw_next"], f32, "dw_next"),
-                0 if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(), _stream(None))
+        args = (self._arg(dresid, rtype, "dresid", (T, H)),
+                self._arg(dx, torch.bfloat16, "dx", (T, H)),
+                self._arg(resid, rtype, "resid", (T, H)),
+                self._arg(y, None if y is None else y.dtype, "y", (T, H)),
+                self._arg(rstd_post, f32, "rstd_post", (T,)),
+                self._arg(rstd_next, f32, "rstd_next", (T,)),
+                self._arg(w_post, f32, "w_post", (H,)), self._arg(gate, f32, "gate", (H,)))
+        pn = self._arg(w_next, f32, "w_next", (H,))
+        types = (_dtype(rtype, "dresid"), MOE_F32 if y is None else _dtype(y, "y"),
+                 _dtype(dy_dtype, "dy_dtype"))
+        vec = lambda v: None if v is None else v.new_empty((H,))  # noqa: E731
+        out = dict(dresid=like.new_empty((T, H)),
+                   dy=like.new_empty((T, H), dtype=dy_dtype) if has_block else None,
+                   dw_post=vec(w_post), dgate=vec(gate), dw_next=vec(w_next))
+        ws = workspace
+        if ws is None and not (w_post is None and gate is None and w_next is None):
+            ws = like.new_empty((self.block_norm_workspace_bytes(T),), dtype=torch.uint8)
+        elif ws is not None and ws.get_device() != self._device_index:
+            raise ValueError(f"workspace must be on cuda:{self._device_index}, got {ws.device}")
+        ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+        st = moe_block_norm_backward(
+            self._h, T, *types, *args, scale, pn, ptr(out["dresid"]), ptr(out["dy"]),
+            ptr(out["dw_post"]), ptr(out["dgate"]), ptr(out["dw_next"]), ptr(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), self._current())
         _check(st, "moe_block_norm_backward")
         return out
 
@@ -428,10 +467,13 @@ class Moe:
         """The layer inside its transformer block: x is the normed residual (block_norm of the
         previous block, or block_norm(resid, w_next=...) before the first), the layer's output goes
         through block_norm into the residual.  Returns block_norm's dict."""
-        with self._on(stream, resid, x):
-            y = self.forward(x, W_router, b_router, W_gate_up, W_down, workspace=workspace)
-            return self.block_norm(resid, y, w_post=w_post, gate=gate, scale=scale, w_next=w_next,
-                                   eps=eps, resid_out=resid_out)
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.block(resid, x, W_router, b_router, W_gate_up, W_down, w_post, gate,
+                                  scale, w_next, eps, resid_out, None, workspace)
+        y = self.forward(x, W_router, b_router, W_gate_up, W_down, workspace=workspace)
+        return self.block_norm(resid, y, w_post=w_post, gate=gate, scale=scale, w_next=w_next,
+                               eps=eps, resid_out=resid_out)
 
     def workspace_bytes_mxfp4(self, T: int) -> int:
         return moe_workspace_bytes_mxfp4(self._h, T)
