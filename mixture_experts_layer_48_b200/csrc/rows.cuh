@@ -44,8 +44,20 @@ MOE_DEVINL float4 fma4(float4 a, float b, float4 c) {
 }
 MOE_DEVINL float dot4(float4 a, float4 b) { return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w; }
 
+// How a row of n4 vectors lies on TPR threads: thread l holds vectors l, l + TPR, ... (VPT of
+// them).  The launch picks (TPR, VPT) so that the first kFull of a thread's vectors exist for
+// every thread; only the last ones are tested against the row's end.
+template <int TPR, int VPT>
+struct RowCfg {
+  static constexpr int kThreads = TPR < 128 ? 128 : TPR;
+  static constexpr int kRows = kThreads / TPR;   // rows per block
+  static constexpr int kFull = VPT <= 4 ? VPT - 1 : VPT == 6 ? 4 : 6;
+  static_assert(VPT <= 4 || VPT == 6 || VPT == 8, "by_row_length");
+};
+
 // Sum over the TPR threads of a row, the same value in each of them.  `red` has a word per warp
-// of the block; every thread of the block takes part.  Two calls in a row alternate `red`.
+// of the block; every thread of the block takes part.  Calls in a row alternate between two such
+// arrays, so that a call's words are read before the next but one overwrites them.
 template <int TPR>
 MOE_DEVINL float row_sum(float v, float* red) {
 #pragma unroll
@@ -63,12 +75,6 @@ MOE_DEVINL float row_sum(float v, float* red) {
   return v;
 }
 
-template <int TPR>
-struct RowCfg {
-  static constexpr int kThreads = TPR < 128 ? 128 : TPR;
-  static constexpr int kRows = kThreads / TPR;   // rows per block
-};
-
 // ---- norms around the block ---------------------------------------------------------------------
 struct NormArgs {
   int T, H;
@@ -85,37 +91,42 @@ struct NormArgs {
   void *dresid_out, *dy;
   int dy_f32;
   float *part_y, *part_x;                   // [row groups, H] partial column sums, or null
+  int stages, stage_bytes;                  // the ring of the staged backward kernel
+  uint32_t* status;
 };
+
+// scale * gate * w_post, all that either pass needs of the three.
+MOE_DEVINL float4 post_factor(const NormArgs& a, int v) {
+  float4 p = make_float4(a.scale, a.scale, a.scale, a.scale);
+  if (a.gate != nullptr) p = p * load4(a.gate + 4 * v);
+  if (a.w_post != nullptr) p = p * load4(a.w_post + 4 * v);
+  return p;
+}
 
 // r' = r + scale * gate * norm(y);  x = norm(r').  RT, YT: float or uint16_t (bf16).
 template <int TPR, int VPT, typename RT, typename YT>
-__global__ void __launch_bounds__(RowCfg<TPR>::kThreads)
+__global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads)
     block_norm_kernel(const NormArgs a) {
-  constexpr int kRows = RowCfg<TPR>::kRows;
-  __shared__ float red[2][RowCfg<TPR>::kThreads / 32];
+  using C = RowCfg<TPR, VPT>;
+  __shared__ float red[2][C::kThreads / 32];
   const int lane = threadIdx.x % TPR;
-  const int t = blockIdx.x * kRows + threadIdx.x / TPR;
-  const bool live = t < a.T;
-  const int nv = live ? a.H / 4 : 0;
-  const size_t base = (size_t)t * a.H;
+  const int t = blockIdx.x * C::kRows + threadIdx.x / TPR;
+  const bool live = C::kRows == 1 || t < a.T;
+  const int n4 = a.H / 4;
+  const size_t base = (size_t)t * a.H + 4 * lane;
   pdl_wait();
   pdl_launch_next();
   const RT* resid = static_cast<const RT*>(a.resid) + base;
   const YT* yrow = static_cast<const YT*>(a.y) + base;
   const float inv_h = 1.f / (float)a.H;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  auto ok = [&](int i) { return live && (i < C::kFull || i * TPR + lane < n4); };
   float4 r[VPT], y[VPT];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = i * TPR + lane;
-    r[i] = v < nv ? load4(resid + 4 * v) : zero;
-  }
+  for (int i = 0; i < VPT; ++i) r[i] = ok(i) ? load4(resid + 4 * i * TPR) : zero;
   if (a.y != nullptr) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * TPR + lane;
-      y[i] = v < nv ? load4(yrow + 4 * v) : zero;
-    }
+    for (int i = 0; i < VPT; ++i) y[i] = ok(i) ? load4(yrow + 4 * i * TPR) : zero;
     float s = 1.f;
     if (a.w_post != nullptr) {
       float ss = 0.f;
@@ -126,17 +137,12 @@ __global__ void __launch_bounds__(RowCfg<TPR>::kThreads)
     }
     RT* out = static_cast<RT*>(a.resid_out) + base;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * TPR + lane;
-      if (v < nv) {
-        float4 n = y[i];
-        if (a.w_post != nullptr) n = n * s * load4(a.w_post + 4 * v);
-        if (a.gate != nullptr) n = n * load4(a.gate + 4 * v);
-        const float4 q = fma4(n, a.scale, r[i]);
-        save4(out + 4 * v, q);
+    for (int i = 0; i < VPT; ++i)
+      if (ok(i)) {
+        const float4 q = fma4(y[i] * s, post_factor(a, i * TPR + lane), r[i]);
+        save4(out + 4 * i * TPR, q);
         r[i] = as_stored(out, q);   // the next norm reads what a reader of r' would
       }
-    }
   }
   if (a.x != nullptr) {
     float ss = 0.f;
@@ -145,11 +151,25 @@ __global__ void __launch_bounds__(RowCfg<TPR>::kThreads)
     const float s = rsqrtf(row_sum<TPR>(ss, red[1]) * inv_h + a.eps);
     if (live && lane == 0) a.rstd_next[t] = s;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * TPR + lane;
-      if (v < nv) save4(a.x + base + 4 * v, r[i] * s * load4(a.w_next + 4 * v));
-    }
+    for (int i = 0; i < VPT; ++i)
+      if (ok(i))
+        save4(a.x + base + 4 * i * TPR, r[i] * s * load4(a.w_next + 4 * (i * TPR + lane)));
   }
+}
+
+// Blocks per SM of the backward kernel: 512 threads (128 registers each) with up to four vectors a
+// thread; longer rows take one block.
+template <int TPR, int VPT>
+constexpr int norm_backward_blocks() {
+  return VPT > 4 ? 1 : 512 / RowCfg<TPR, VPT>::kThreads;
+}
+constexpr int kRowRingMax = 4;
+
+// Thread 0: `rows` rows of row_bytes from g (null: none) to a stage, counted on its barrier.
+MOE_DEVINL void ring_copy(uint8_t* to, const void* g, size_t row0, int rows, int row_bytes,
+                          uint64_t* bar) {
+  if (g != nullptr)
+    bulk_g2s(to, static_cast<const uint8_t*>(g) + row0 * row_bytes, rows * row_bytes, bar);
 }
 
 // Backward.  With rh = r' * rstd_next and t = dx * w_next:
@@ -157,115 +177,172 @@ __global__ void __launch_bounds__(RowCfg<TPR>::kThreads)
 // with yh = y * rstd_post (or y without the norm after) and d = scale * gate * dr * w_post:
 //   dy = rstd_post * (d - yh * mean(d * yh))                          (or scale * gate * dr)
 // column sums: part_x = sum dx * rh (dw_next), part_y = sum dr * yh (dw_post and dgate follow).
-template <int TPR, int VPT, typename RT, typename YT>
-__global__ void __launch_bounds__(RowCfg<TPR>::kThreads, TPR <= 128 ? 3 : 1)
+//
+// Persistent blocks: the column sums stay in registers over all rows of a block.  STAGED: a
+// block's next rows are on their way while it works on one, a bulk copy per operand into a ring
+// of shared-memory stages, read into registers at the start of a step and refilled after the
+// step's first block-wide barrier; the vectors are then held in registers too (the ring leaves
+// too little L1 for them: loaded again for every row they cost more time than the row itself).
+// Rows too long for a ring and those registers come straight from global memory.
+template <int TPR, int VPT, typename RT, typename YT, bool STAGED>
+__global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads, norm_backward_blocks<TPR, VPT>())
     block_norm_backward_kernel(const NormArgs a) {
-  constexpr int kRows = RowCfg<TPR>::kRows;
-  __shared__ float red[2][RowCfg<TPR>::kThreads / 32];
+  using C = RowCfg<TPR, VPT>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[2][C::kThreads / 32];
+  __shared__ uint64_t full[kRowRingMax];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int n4 = a.H / 4;
   const float inv_h = 1.f / (float)a.H;
   const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  float4 sum_x[VPT], sum_y[VPT];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) sum_x[i] = sum_y[i] = zero;
+  const int r_bytes = a.H * (int)sizeof(RT), y_bytes = a.H * (int)sizeof(YT), x_bytes = a.H * 2;
+  const int step = gridDim.x * C::kRows;
+  auto fetch = [&](int t0, int slot) {   // thread 0
+    const int rows = min(C::kRows, a.T - t0);
+    uint64_t* bar = &full[slot];
+    mbar_arrive_expect_tx(bar, rows * ((a.dresid != nullptr ? r_bytes : 0) +
+                                       (a.dx != nullptr ? x_bytes + r_bytes : 0) +
+                                       (a.y != nullptr ? y_bytes : 0)));
+    uint8_t* stage = ring + slot * a.stage_bytes;
+    ring_copy(stage, a.dresid, t0, rows, r_bytes, bar);
+    ring_copy(stage + C::kRows * r_bytes, a.dx != nullptr ? a.resid : nullptr, t0, rows, r_bytes, bar);
+    ring_copy(stage + 2 * C::kRows * r_bytes, a.dx, t0, rows, x_bytes, bar);
+    ring_copy(stage + C::kRows * (2 * r_bytes + x_bytes), a.y, t0, rows, y_bytes, bar);
+  };
+  if (STAGED && threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
   pdl_wait();
   pdl_launch_next();
+  if (STAGED) {
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int s = 0, t0 = blockIdx.x * C::kRows; s < a.stages && t0 < a.T; ++s, t0 += step)
+        fetch(t0, s);
+  }
+  constexpr int kHeld = STAGED ? VPT : 1;
+  float4 w_next[kHeld], w_post[kHeld];
+  float4 sum_x[VPT], sum_y[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = i * TPR + lane;
+    sum_x[i] = sum_y[i] = zero;
+    if (STAGED) {
+      w_next[i] = a.w_next != nullptr && v < n4 ? load4(a.w_next + 4 * v) : zero;
+      w_post[i] = v < n4 ? post_factor(a, v) : zero;
+    }
+  }
+  auto next_factor = [&](int i) { return STAGED ? w_next[i] : load4(a.w_next + 4 * (i * TPR + lane)); };
+  auto y_factor = [&](int i) { return STAGED ? w_post[i] : post_factor(a, i * TPR + lane); };
+
   // every thread of the block takes every step (the row sums are block-wide)
-  for (int t0 = blockIdx.x * kRows; t0 < a.T; t0 += gridDim.x * kRows) {
+  int slot = 0, turn = 0;
+  uint32_t phase = 0;
+  bool gave_up = false;   // a copy did not arrive: the status word says so, the rest is not waited for
+  for (int t0 = blockIdx.x * C::kRows; t0 < a.T; t0 += step) {
     const int t = t0 + sub;
-    const bool live = t < a.T;
-    const int nv = live ? a.H / 4 : 0;
-    const size_t base = (size_t)t * a.H;
+    const bool live = C::kRows == 1 || t < a.T;
+    auto ok = [&](int i) { return live && (i < C::kFull || i * TPR + lane < n4); };
+    const size_t base = (size_t)t * a.H + 4 * lane;
     float4 dr[VPT], dx[VPT], r[VPT], y[VPT];
     const RT* dres = static_cast<const RT*>(a.dresid) + base;
     const RT* res = static_cast<const RT*>(a.resid) + base;
+    const uint16_t* dxrow = a.dx + base;
     const YT* yrow = static_cast<const YT*>(a.y) + base;
-    const bool need_y = a.y != nullptr;
+    if (STAGED) {
+      if (!gave_up && !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs)) {
+        atomicOr(a.status, kStatusTimeout);
+        gave_up = true;
+      }
+      const uint8_t* stage = ring + slot * a.stage_bytes;
+      const int at = sub * a.H + 4 * lane;
+      dres = reinterpret_cast<const RT*>(stage) + at;
+      res = reinterpret_cast<const RT*>(stage + C::kRows * r_bytes) + at;
+      dxrow = reinterpret_cast<const uint16_t*>(stage + 2 * C::kRows * r_bytes) + at;
+      yrow = reinterpret_cast<const YT*>(stage + C::kRows * (2 * r_bytes + x_bytes)) + at;
+    }
+    // A barrier after the loads: the stage may be refilled.  The first row sum of a step is one.
+    auto refill = [&]() {
+      if (STAGED) {
+        if (threadIdx.x == 0 && !gave_up && t0 + (long long)a.stages * step < a.T)
+          fetch(t0 + a.stages * step, slot);
+        if (++slot == a.stages) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    };
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * TPR + lane;
-      dr[i] = a.dresid != nullptr && v < nv ? load4(dres + 4 * v) : zero;
+    for (int i = 0; i < VPT; ++i) dr[i] = a.dresid != nullptr && ok(i) ? load4(dres + 4 * i * TPR) : zero;
+    if (a.y != nullptr) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) y[i] = ok(i) ? load4(yrow + 4 * i * TPR) : zero;
     }
     if (a.dx != nullptr) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + lane;
-        dx[i] = v < nv ? load4(a.dx + base + 4 * v) : zero;
-        r[i] = v < nv ? load4(res + 4 * v) : zero;
+        dx[i] = ok(i) ? load4(dxrow + 4 * i * TPR) : zero;
+        r[i] = ok(i) ? load4(res + 4 * i * TPR) : zero;
       }
-    }
-    if (need_y) {
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + lane;
-        y[i] = v < nv ? load4(yrow + 4 * v) : zero;
-      }
-    }
-    if (a.dx != nullptr) {
       const float s = live ? a.c_rstd_next[t] : 0.f;
       float c = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + lane;
-        if (v < nv) {
+      for (int i = 0; i < VPT; ++i)
+        if (ok(i)) {
           r[i] = r[i] * s;
           sum_x[i] = fma4(dx[i], r[i], sum_x[i]);
-          dx[i] = dx[i] * load4(a.w_next + 4 * v);
+          dx[i] = dx[i] * next_factor(i);
           c += dot4(dx[i], r[i]);
         }
-      }
-      c = row_sum<TPR>(c, red[0]) * inv_h;
+      c = row_sum<TPR>(c, red[turn]) * inv_h;
+      turn ^= 1;
+      if (TPR == 32) __syncthreads();
+      refill();
 #pragma unroll
       for (int i = 0; i < VPT; ++i) dr[i] = fma4(fma4(r[i], -c, dx[i]), s, dr[i]);
+    } else {
+      __syncthreads();
+      refill();
     }
     RT* out = static_cast<RT*>(a.dresid_out) + base;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = i * TPR + lane;
-      if (v < nv) save4(out + 4 * v, dr[i]);
-    }
+    for (int i = 0; i < VPT; ++i)
+      if (ok(i)) save4(out + 4 * i * TPR, dr[i]);
     if (a.dy != nullptr) {
       const float s = a.w_post != nullptr && live ? a.c_rstd_post[t] : 1.f;
       float c = 0.f;
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + lane;
-        if (v < nv) {
-          if (need_y) {
+      for (int i = 0; i < VPT; ++i)
+        if (ok(i)) {
+          if (a.y != nullptr) {
             y[i] = y[i] * s;
             sum_y[i] = fma4(dr[i], y[i], sum_y[i]);
           }
-          dr[i] = dr[i] * a.scale;
-          if (a.gate != nullptr) dr[i] = dr[i] * load4(a.gate + 4 * v);
-          if (a.w_post != nullptr) {
-            dr[i] = dr[i] * load4(a.w_post + 4 * v);
-            c += dot4(dr[i], y[i]);
-          }
+          dr[i] = dr[i] * y_factor(i);
+          if (a.w_post != nullptr) c += dot4(dr[i], y[i]);
         }
-      }
       if (a.w_post != nullptr) {
-        c = row_sum<TPR>(c, red[1]) * inv_h;
+        c = row_sum<TPR>(c, red[turn]) * inv_h;
+        turn ^= 1;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) dr[i] = fma4(y[i], -c, dr[i]) * s;
       }
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = i * TPR + lane;
-        if (v < nv) {
-          if (a.dy_f32) save4(static_cast<float*>(a.dy) + base + 4 * v, dr[i]);
-          else save4(static_cast<uint16_t*>(a.dy) + base + 4 * v, dr[i]);
+      for (int i = 0; i < VPT; ++i)
+        if (ok(i)) {
+          if (a.dy_f32) save4(static_cast<float*>(a.dy) + base + 4 * i * TPR, dr[i]);
+          else save4(static_cast<uint16_t*>(a.dy) + base + 4 * i * TPR, dr[i]);
         }
-      }
     }
-    // the next row's first row_sum must not overwrite words that a slower warp still reads:
-    // a row that takes one sum has no second barrier in between
-    if (TPR > 32) __syncthreads();
   }
-  const size_t row = (size_t)(blockIdx.x * kRows + sub) * a.H;
+  if (STAGED && gave_up && threadIdx.x == 0)   // what is still on its way must land first
+    for (int s = 0; s < a.stages; ++s) mbar_wait_bounded(&full[s], s < slot ? phase ^ 1u : phase, kWaitLimitNs);
+  const size_t row = (size_t)(blockIdx.x * C::kRows + sub) * a.H;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = i * TPR + lane;
-    if (v < a.H / 4) {
+    if (v < n4) {
       if (a.part_x != nullptr) save4(a.part_x + row + 4 * v, sum_x[i]);
       if (a.part_y != nullptr) save4(a.part_y + row + 4 * v, sum_y[i]);
     }
@@ -273,14 +350,14 @@ __global__ void __launch_bounds__(RowCfg<TPR>::kThreads, TPR <= 128 ? 3 : 1)
 }
 
 // dw_next[h] = sum_p part_x[p, h]; with S[h] = sum_p part_y[p, h]: dw_post = scale * gate * S and
-// dgate = scale * w_post * S.  block 256 = 32 columns x 8 slices of the partial rows, each slice
+// dgate = scale * w_post * S.  block 1024 = 32 columns x 32 slices of the partial rows, each slice
 // added in row order, then the slices in order.  grid (ceil(H / 32), 2).
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(1024)
     block_norm_colsum_kernel(const float* __restrict__ part_x, const float* __restrict__ part_y,
                              int parts, int H, float scale, const float* __restrict__ gate,
                              const float* __restrict__ w_post, float* __restrict__ dw_next,
                              float* __restrict__ dw_post, float* __restrict__ dgate) {
-  __shared__ float acc[8][33];
+  __shared__ float acc[32][33];
   pdl_wait();
   pdl_launch_next();
   const float* part = blockIdx.y == 0 ? part_x : part_y;
@@ -289,15 +366,15 @@ __global__ void __launch_bounds__(256)
   const int h = blockIdx.x * 32 + lane;
   float s = 0.f;
   if (h < H) {
-    const int per = (parts + 7) / 8, p1 = min(parts, (slice + 1) * per);
-#pragma unroll 8
+    const int per = (parts + 31) / 32, p1 = min(parts, (slice + 1) * per);
+#pragma unroll 4
     for (int p = slice * per; p < p1; ++p) s += part[(size_t)p * H + h];
   }
   acc[slice][lane] = s;
   __syncthreads();
   if (slice != 0 || h >= H) return;
 #pragma unroll
-  for (int i = 1; i < 8; ++i) s += acc[i][lane];
+  for (int i = 1; i < 32; ++i) s += acc[i][lane];
   if (blockIdx.y == 0) {
     dw_next[h] = s;
     return;
@@ -335,12 +412,12 @@ __global__ void __launch_bounds__(256)
 
 // With s = sigmoid(g): du = w dh g s;  dg = w dh u s (1 + g (1 - s));  dw = sum dh g s u.
 template <int TPR, int VPT>
-__global__ void __launch_bounds__(RowCfg<TPR>::kThreads)
+__global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads)
     swiglu_rows_backward_kernel(const uint16_t* __restrict__ dh, const uint16_t* __restrict__ gu,
                                 const float* __restrict__ row_w, uint16_t* __restrict__ dgu,
                                 float* __restrict__ drow_w, int R, int I) {
-  constexpr int kRows = RowCfg<TPR>::kRows;
-  __shared__ float red[RowCfg<TPR>::kThreads / 32];
+  constexpr int kRows = RowCfg<TPR, VPT>::kRows;
+  __shared__ float red[RowCfg<TPR, VPT>::kThreads / 32];
   const int lane = threadIdx.x % TPR;
   const int r = blockIdx.x * kRows + threadIdx.x / TPR;
   const bool live = r < R;

@@ -78,13 +78,6 @@ bool set_grouped_attrs() {
          smem_attr(grouped_rows_kernel<TRANS, F32>, kPairSmem);
 }
 
-bool set_rows_smem_attrs() {
-  return set_grouped_attrs<false, false>() && set_grouped_attrs<false, true>() &&
-         set_grouped_attrs<true, false>() && set_grouped_attrs<true, true>() &&
-         smem_attr(grouped_wgrad_kernel<false>, kPairSmem) &&
-         smem_attr(grouped_wgrad_kernel<true>, kPairSmem);
-}
-
 // Clusters of 2 and 4 CTAs of the few-row kernel (one CTA per SM) that fit the GPU at once: a
 // cluster lies inside one GPC, whose SM count need not be a multiple of its size.
 bool query_clusters(int num_sms, int* out) {
@@ -208,17 +201,29 @@ bool grouped_shape_ok(const moe_ctx* c, int R, int K, int N, moe_dtype out_type)
 }
 
 // ---- row kernels: threads per row from the row's length ------------------------------------------
-// f<TPR, VPT4>(): TPR threads hold VPT4 vectors of 4 elements each of a row of n elements.
-// 6 vectors keep a row of 2880 on 128 threads at 94 % use, with every load of the row in flight.
+// f(TPR, VPT) for a row of n4 vectors: the fewest threads (up to 512) that hold it with three
+// vectors each, two where they suffice.  Rows beyond that take more vectors.
 template <typename F>
-moe_status by_row_length(int n, F&& f) {
+moe_status by_row_length(int n4, F&& f) {
   using std::integral_constant;
-  if (n <= 24 * 32) return f(integral_constant<int, 32>{}, integral_constant<int, 6>{});
-  if (n <= 24 * 64) return f(integral_constant<int, 64>{}, integral_constant<int, 6>{});
-  if (n <= 24 * 128) return f(integral_constant<int, 128>{}, integral_constant<int, 6>{});
-  if (n <= 24 * 256) return f(integral_constant<int, 256>{}, integral_constant<int, 6>{});
-  if (n <= 24 * 512) return f(integral_constant<int, 512>{}, integral_constant<int, 6>{});
-  return f(integral_constant<int, 512>{}, integral_constant<int, 8>{});
+  auto pick = [&](auto tpr, auto vpt) { return f(tpr, vpt); };
+#define MOE_ROW(tpr, vpt) \
+  if (n4 <= tpr * vpt) return pick(integral_constant<int, tpr>{}, integral_constant<int, vpt>{})
+  MOE_ROW(32, 1);
+  MOE_ROW(32, 2);
+  MOE_ROW(32, 3);
+  MOE_ROW(64, 2);
+  MOE_ROW(64, 3);
+  MOE_ROW(128, 2);
+  MOE_ROW(128, 3);
+  MOE_ROW(256, 2);
+  MOE_ROW(256, 3);
+  MOE_ROW(512, 2);
+  MOE_ROW(512, 3);
+  MOE_ROW(512, 4);
+  MOE_ROW(512, 6);
+#undef MOE_ROW
+  return pick(integral_constant<int, 512>{}, integral_constant<int, 8>{});
 }
 
 template <typename F>
@@ -230,23 +235,74 @@ moe_status by_types(moe_dtype resid_type, moe_dtype y_type, F&& f) {
 
 bool dtype_ok(moe_dtype t) { return t == MOE_BF16 || t == MOE_F32; }
 
-// Persistent blocks of the backward norm: three fit an SM up to 128 threads a row (at most 170
-// registers a thread), else one.
-template <int TPR>
-int norm_backward_blocks(const moe_ctx* c, int T) {
-  const long long need = ((long long)T + RowCfg<TPR>::kRows - 1) / RowCfg<TPR>::kRows;
-  return (int)std::min<long long>(need, (long long)c->num_sms * (TPR <= 128 ? 3 : 1));
+// Ring of the staged backward norm: blocks per SM and stages.  The most bytes in flight that fit
+// an SM's shared memory; one stage where two of one block do not fit.
+struct RowPlan {
+  int blocks, stages;
+};
+RowPlan plan_rows(int stage_bytes, int max_blocks) {
+  const int budget = 224 * 1024, fixed = 1280;   // an SM's; a block's reserve and static part
+  RowPlan best{1, 1};
+  long long most = 0;
+  for (int b = 1; b <= max_blocks; ++b)
+    for (int s = 2; s <= kRowRingMax; ++s) {
+      const long long bytes = (long long)b * s * stage_bytes;
+      if (bytes + b * fixed <= budget && bytes >= most) {
+        most = bytes;
+        best = {b, s};
+      }
+    }
+  return best;
 }
 
-// Partial rows of each column sum.
+// Persistent blocks of a call.
+template <int TPR, int VPT>
+int row_grid(const moe_ctx* c, int T, int blocks) {
+  const long long need = ((long long)T + RowCfg<TPR, VPT>::kRows - 1) / RowCfg<TPR, VPT>::kRows;
+  return (int)std::min<long long>(need, (long long)c->num_sms * blocks);
+}
+
+// Most partial rows that a column sum of T rows can have.
 int norm_backward_parts(const moe_ctx* c, int T) {
   int parts = 0;
-  by_row_length(c->H, [&](auto tpr, auto) {
-    constexpr int TPR = decltype(tpr)::value;
-    parts = norm_backward_blocks<TPR>(c, T) * RowCfg<TPR>::kRows;
+  by_row_length(c->H / 4, [&](auto tpr, auto vpt) {
+    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+    parts = row_grid<TPR, VPT>(c, T, norm_backward_blocks<TPR, VPT>()) * RowCfg<TPR, VPT>::kRows;
     return MOE_OK;
   });
   return parts;
+}
+
+// The staged kernel holds its vectors and sums in registers: up to four vectors a thread.
+template <int VPT>
+constexpr bool norm_staged() { return VPT <= 4; }
+
+bool set_row_attrs() {
+  for (int n4 = 16; n4 <= kMaxHI / 4; n4 += 16)
+    for (moe_dtype r : {MOE_BF16, MOE_F32})
+      for (moe_dtype y : {MOE_BF16, MOE_F32}) {
+        static_assert(kMaxHI % 64 == 0, "");
+        const moe_status s = by_row_length(n4, [&](auto tpr, auto vpt) {
+          constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+          if (!norm_staged<VPT>() || n4 != TPR * VPT) return MOE_OK;   // each variant once
+          return by_types(r, y, [&](auto rt, auto yt) {
+            return smem_attr(block_norm_backward_kernel<TPR, VPT, decltype(rt), decltype(yt),
+                                                        norm_staged<VPT>()>,
+                             222 * 1024)
+                       ? MOE_OK
+                       : MOE_ERR_CUDA;
+          });
+        });
+        if (s != MOE_OK) return false;
+      }
+  return true;
+}
+
+bool set_rows_smem_attrs() {
+  return set_grouped_attrs<false, false>() && set_grouped_attrs<false, true>() &&
+         set_grouped_attrs<true, false>() && set_grouped_attrs<true, true>() &&
+         smem_attr(grouped_wgrad_kernel<false>, kPairSmem) &&
+         smem_attr(grouped_wgrad_kernel<true>, kPairSmem) && set_row_attrs();
 }
 
 }  // namespace
@@ -331,12 +387,13 @@ moe_status moe_swiglu_backward(moe_t c, int R, const void* dh_bf16, const void* 
       !all_aligned16({dh_bf16, gu_bf16, row_w, dgu_bf16, drow_w}) || !on_device(c))
     return MOE_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  return by_row_length(c->I, [&](auto tpr, auto vpt) {
-    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value / 2;
-    const int rows = RowCfg<TPR>::kRows;
+  return by_row_length(c->I / 8, [&](auto tpr, auto vpt) {   // vectors of 8
+    constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+    const int rows = RowCfg<TPR, VPT>::kRows;
     return launch(c, -1, st, [&] {
       return launch_pdl(swiglu_rows_backward_kernel<TPR, VPT>, dim3((R + rows - 1) / rows),
-                        dim3(RowCfg<TPR>::kThreads), 0, st, static_cast<const uint16_t*>(dh_bf16),
+                        dim3(RowCfg<TPR, VPT>::kThreads), 0, st,
+                        static_cast<const uint16_t*>(dh_bf16),
                         static_cast<const uint16_t*>(gu_bf16), row_w,
                         static_cast<uint16_t*>(dgu_bf16), drow_w, R, c->I);
     });
@@ -373,13 +430,13 @@ moe_status moe_block_norm(moe_t c, int T, moe_dtype resid_type, moe_dtype y_type
   a.x = static_cast<uint16_t*>(x_bf16);
   a.rstd_post = rstd_post;
   a.rstd_next = rstd_next;
-  return by_row_length(c->H, [&](auto tpr, auto vpt) {
+  return by_row_length(c->H / 4, [&](auto tpr, auto vpt) {
     constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
     return by_types(resid_type, y_type, [&](auto rt, auto yt) {
-      const int rows = RowCfg<TPR>::kRows;
+      const int rows = RowCfg<TPR, VPT>::kRows;
       return launch(c, -1, st, [&] {
         return launch_pdl(block_norm_kernel<TPR, VPT, decltype(rt), decltype(yt)>,
-                          dim3((T + rows - 1) / rows), dim3(RowCfg<TPR>::kThreads), 0, st, a);
+                          dim3((T + rows - 1) / rows), dim3(RowCfg<TPR, VPT>::kThreads), 0, st, a);
       });
     });
   });
@@ -418,9 +475,11 @@ moe_status moe_block_norm_backward(moe_t c, int T, moe_dtype resid_type, moe_dty
   if (sums && (!workspace || !aligned16(workspace) || ws_bytes < moe_block_norm_workspace_bytes(c, T)))
     return MOE_ERR_WORKSPACE;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  const int parts = norm_backward_parts(c, T);
   float* part_x = next ? static_cast<float*>(workspace) : nullptr;
-  float* part_y = post || gated ? static_cast<float*>(workspace) + (size_t)parts * c->H : nullptr;
+  float* part_y = post || gated ? static_cast<float*>(workspace) +
+                                      (size_t)norm_backward_parts(c, T) * c->H
+                                : nullptr;
+  int parts = 0;   // partial rows that this call writes
   if (T > 0) {
     NormArgs a{};
     a.T = T;
@@ -440,20 +499,31 @@ moe_status moe_block_norm_backward(moe_t c, int T, moe_dtype resid_type, moe_dty
     a.dy_f32 = dy_type == MOE_F32;
     a.part_x = part_x;
     a.part_y = part_y;
-    MOE_TRY(by_row_length(c->H, [&](auto tpr, auto vpt) {
+    a.status = c->d_status;
+    MOE_TRY(by_row_length(c->H / 4, [&](auto tpr, auto vpt) {
       constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
+      using C = RowCfg<TPR, VPT>;
       return by_types(resid_type, y_type, [&](auto rt, auto yt) {
+        using RT = decltype(rt);
+        using YT = decltype(yt);
+        RowPlan p{norm_backward_blocks<TPR, VPT>(), 0};
+        if (norm_staged<VPT>()) {
+          a.stage_bytes = C::kRows * c->H * (int)(2 * sizeof(RT) + 2 + (a.y ? sizeof(YT) : 0));
+          p = plan_rows(a.stage_bytes, p.blocks);
+          a.stages = p.stages;
+        }
+        const int grid = row_grid<TPR, VPT>(c, T, p.blocks);
+        parts = grid * C::kRows;
         return launch(c, -1, st, [&] {
-          return launch_pdl(block_norm_backward_kernel<TPR, VPT, decltype(rt), decltype(yt)>,
-                            dim3(norm_backward_blocks<TPR>(c, T)), dim3(RowCfg<TPR>::kThreads), 0,
-                            st, a);
+          return launch_pdl(block_norm_backward_kernel<TPR, VPT, RT, YT, norm_staged<VPT>()>,
+                            dim3(grid), dim3(C::kThreads), (size_t)a.stages * a.stage_bytes, st, a);
         });
       });
     }));
   }
   if (!sums) return MOE_OK;
   return launch(c, -1, st, [&] {
-    return launch_pdl(block_norm_colsum_kernel, dim3((c->H + 31) / 32, 2), dim3(256), 0, st,
+    return launch_pdl(block_norm_colsum_kernel, dim3((c->H + 31) / 32, 2), dim3(1024), 0, st,
                       (const float*)part_x, (const float*)part_y, parts, c->H, scale, gate, w_post,
                       dw_next, dw_post, dgate);
   });
