@@ -91,7 +91,7 @@ struct NormArgs {
   void *dresid_out, *dy;
   int dy_f32;
   float *part_y, *part_x;                   // [row groups, H] partial column sums, or null
-  int stages, stage_bytes;                  // the ring of the staged backward kernel
+  int stages, stage_bytes;                  // the ring of the staged kernels
   uint32_t* status;
 };
 
@@ -103,65 +103,15 @@ MOE_DEVINL float4 post_factor(const NormArgs& a, int v) {
   return p;
 }
 
-// r' = r + scale * gate * norm(y);  x = norm(r').  RT, YT: float or uint16_t (bf16).
-template <int TPR, int VPT, typename RT, typename YT>
-__global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads)
-    block_norm_kernel(const NormArgs a) {
-  using C = RowCfg<TPR, VPT>;
-  __shared__ float red[2][C::kThreads / 32];
-  const int lane = threadIdx.x % TPR;
-  const int t = blockIdx.x * C::kRows + threadIdx.x / TPR;
-  const bool live = C::kRows == 1 || t < a.T;
-  const int n4 = a.H / 4;
-  const size_t base = (size_t)t * a.H + 4 * lane;
-  pdl_wait();
-  pdl_launch_next();
-  const RT* resid = static_cast<const RT*>(a.resid) + base;
-  const YT* yrow = static_cast<const YT*>(a.y) + base;
-  const float inv_h = 1.f / (float)a.H;
-  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto ok = [&](int i) { return live && (i < C::kFull || i * TPR + lane < n4); };
-  float4 r[VPT], y[VPT];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) r[i] = ok(i) ? load4(resid + 4 * i * TPR) : zero;
-  if (a.y != nullptr) {
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) y[i] = ok(i) ? load4(yrow + 4 * i * TPR) : zero;
-    float s = 1.f;
-    if (a.w_post != nullptr) {
-      float ss = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) ss += dot4(y[i], y[i]);
-      s = rsqrtf(row_sum<TPR>(ss, red[0]) * inv_h + a.eps);
-      if (live && lane == 0) a.rstd_post[t] = s;
-    }
-    RT* out = static_cast<RT*>(a.resid_out) + base;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (ok(i)) {
-        const float4 q = fma4(y[i] * s, post_factor(a, i * TPR + lane), r[i]);
-        save4(out + 4 * i * TPR, q);
-        r[i] = as_stored(out, q);   // the next norm reads what a reader of r' would
-      }
-  }
-  if (a.x != nullptr) {
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) ss += dot4(r[i], r[i]);
-    const float s = rsqrtf(row_sum<TPR>(ss, red[1]) * inv_h + a.eps);
-    if (live && lane == 0) a.rstd_next[t] = s;
-#pragma unroll
-    for (int i = 0; i < VPT; ++i)
-      if (ok(i))
-        save4(a.x + base + 4 * i * TPR, r[i] * s * load4(a.w_next + 4 * (i * TPR + lane)));
-  }
+// Blocks per SM of the staged kernels: 1024 threads forward (64 registers each) and 512 backward
+// (128) with up to three vectors a thread, else one block.
+template <int TPR, int VPT>
+constexpr int norm_forward_blocks() {
+  return VPT > 3 ? 1 : 1024 / RowCfg<TPR, VPT>::kThreads;
 }
-
-// Blocks per SM of the backward kernel: 512 threads (128 registers each) with up to four vectors a
-// thread; longer rows take one block.
 template <int TPR, int VPT>
 constexpr int norm_backward_blocks() {
-  return VPT > 4 ? 1 : 512 / RowCfg<TPR, VPT>::kThreads;
+  return VPT > 3 ? 1 : 512 / RowCfg<TPR, VPT>::kThreads;
 }
 constexpr int kRowRingMax = 4;
 
@@ -170,6 +120,136 @@ MOE_DEVINL void ring_copy(uint8_t* to, const void* g, size_t row0, int rows, int
                           uint64_t* bar) {
   if (g != nullptr)
     bulk_g2s(to, static_cast<const uint8_t*>(g) + row0 * row_bytes, rows * row_bytes, bar);
+}
+
+// r' = r + scale * gate * norm(y);  x = norm(r').  RT, YT: float or uint16_t (bf16).  One row a
+// block (or kRows) from global memory; STAGED: persistent blocks that work as the backward kernel's.
+template <int TPR, int VPT, typename RT, typename YT, bool STAGED>
+__global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads,
+                                  STAGED ? norm_forward_blocks<TPR, VPT>() : 1)
+    block_norm_kernel(const NormArgs a) {
+  using C = RowCfg<TPR, VPT>;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float red[2][C::kThreads / 32];
+  __shared__ uint64_t full[kRowRingMax];
+  const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int n4 = a.H / 4;
+  const float inv_h = 1.f / (float)a.H;
+  const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int r_bytes = a.H * (int)sizeof(RT), y_bytes = a.H * (int)sizeof(YT);
+  const int step = gridDim.x * C::kRows;
+  auto fetch = [&](int t0, int slot) {   // thread 0
+    const int rows = min(C::kRows, a.T - t0);
+    uint64_t* bar = &full[slot];
+    mbar_arrive_expect_tx(bar, rows * (r_bytes + (a.y != nullptr ? y_bytes : 0)));
+    uint8_t* stage = ring + slot * a.stage_bytes;
+    ring_copy(stage, a.resid, t0, rows, r_bytes, bar);
+    ring_copy(stage + C::kRows * r_bytes, a.y, t0, rows, y_bytes, bar);
+  };
+  if (STAGED && threadIdx.x == 0) {
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+    fence_barrier_init();
+  }
+  pdl_wait();
+  pdl_launch_next();
+  if (STAGED) {
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int s = 0, t0 = blockIdx.x * C::kRows; s < a.stages && t0 < a.T; ++s, t0 += step)
+        fetch(t0, s);
+  }
+  constexpr int kHeld = STAGED ? VPT : 1;
+  float4 w_next[kHeld], w_post[kHeld];
+  if (STAGED) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = i * TPR + lane;
+      w_next[i] = a.w_next != nullptr && v < n4 ? load4(a.w_next + 4 * v) : zero;
+      w_post[i] = v < n4 ? post_factor(a, v) : zero;
+    }
+  }
+  auto next_factor = [&](int i) { return STAGED ? w_next[i] : load4(a.w_next + 4 * (i * TPR + lane)); };
+  auto y_factor = [&](int i) { return STAGED ? w_post[i] : post_factor(a, i * TPR + lane); };
+
+  int slot = 0, turn = 0;
+  uint32_t phase = 0;
+  bool gave_up = false;
+  int t0 = blockIdx.x * C::kRows;
+  do {
+    const int t = t0 + sub;
+    const bool live = C::kRows == 1 || t < a.T;
+    auto ok = [&](int i) { return live && (i < C::kFull || i * TPR + lane < n4); };
+    const size_t base = (size_t)t * a.H + 4 * lane;
+    const RT* resid = static_cast<const RT*>(a.resid) + base;
+    const YT* yrow = static_cast<const YT*>(a.y) + base;
+    if (STAGED) {
+      if (!gave_up && !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs)) {
+        atomicOr(a.status, kStatusTimeout);
+        gave_up = true;
+      }
+      const uint8_t* stage = ring + slot * a.stage_bytes;
+      const int at = sub * a.H + 4 * lane;
+      resid = reinterpret_cast<const RT*>(stage) + at;
+      yrow = reinterpret_cast<const YT*>(stage + C::kRows * r_bytes) + at;
+    }
+    bool refilled = !STAGED;
+    auto refill = [&]() {   // after a barrier that follows the loads
+      if (refilled) return;
+      refilled = true;
+      if (threadIdx.x == 0 && !gave_up && t0 + (long long)a.stages * step < a.T)
+        fetch(t0 + a.stages * step, slot);
+      if (++slot == a.stages) {
+        slot = 0;
+        phase ^= 1u;
+      }
+    };
+    float4 r[VPT], y[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) r[i] = ok(i) ? load4(resid + 4 * i * TPR) : zero;
+    if (a.y != nullptr) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) y[i] = ok(i) ? load4(yrow + 4 * i * TPR) : zero;
+      float s = 1.f;
+      if (a.w_post != nullptr) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) ss += dot4(y[i], y[i]);
+        s = rsqrtf(row_sum<TPR>(ss, red[turn]) * inv_h + a.eps);
+        turn ^= 1;
+        if (STAGED && TPR == 32) __syncthreads();
+        refill();
+        if (live && lane == 0) a.rstd_post[t] = s;
+      }
+      RT* out = static_cast<RT*>(a.resid_out) + base;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (ok(i)) {
+          const float4 q = fma4(y[i] * s, y_factor(i), r[i]);
+          save4(out + 4 * i * TPR, q);
+          r[i] = as_stored(out, q);   // the next norm reads what a reader of r' would
+        }
+    }
+    if (a.x != nullptr) {
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) ss += dot4(r[i], r[i]);
+      const float s = rsqrtf(row_sum<TPR>(ss, red[turn]) * inv_h + a.eps);
+      turn ^= 1;
+      if (STAGED && TPR == 32) __syncthreads();
+      refill();
+      if (live && lane == 0) a.rstd_next[t] = s;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+        if (ok(i)) save4(a.x + base + 4 * i * TPR, r[i] * s * next_factor(i));
+    }
+    if (STAGED && a.w_post == nullptr && a.x == nullptr) {
+      __syncthreads();
+      refill();
+    }
+    t0 += step;
+  } while (STAGED && t0 < a.T);
+  if (STAGED && gave_up && threadIdx.x == 0)   // what is still on its way must land first
+    for (int s = 0; s < a.stages; ++s) mbar_wait_bounded(&full[s], s < slot ? phase ^ 1u : phase, kWaitLimitNs);
 }
 
 // Backward.  With rh = r' * rstd_next and t = dx * w_next:

@@ -172,6 +172,17 @@ def test_norm_before_the_first_block(T, H, rt):
     _forward_case(T, H, rt, None, False, False, True, seed=T)
 
 
+# more rows than the persistent blocks hold at once, several times over: every ring slot is refilled
+LONG = [(20011, 64), (15013, 192), (9001, 384), (6007, 640), (5003, 1088), (6001, 2880), (3001, 6016), (1501, 8128)]
+
+
+@pytest.mark.parametrize("rt,yt", [(BF16, F32), (BF16, BF16), (F32, BF16), (F32, F32)])
+@pytest.mark.parametrize("post,nxt", [(True, True), (False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("T,H", LONG)
+def test_block_norm_many_rows(T, H, rt, yt, post, nxt):
+    _forward_case(T, H, rt, yt, post, True, nxt, seed=T)
+
+
 @pytest.mark.parametrize("rt", [BF16, F32])
 def test_block_norm_in_place(rt):
     _forward_case(77, 2880, rt, F32, True, True, True, seed=3, inplace=True)
@@ -236,6 +247,13 @@ def _backward_case(T, H, rt, yt, post, gate, nxt, dyt=BF16, scale=0.5, seed=0, d
 @pytest.mark.parametrize("T,H", SIZES)
 def test_block_norm_backward(T, H, rt, yt, post, gate, nxt):
     _backward_case(T, H, rt, yt, post, gate, nxt, dyt=BF16 if T % 2 else F32, seed=T + H)
+
+
+@pytest.mark.parametrize("rt,yt", [(BF16, F32), (F32, BF16), (F32, F32)])
+@pytest.mark.parametrize("post,nxt", [(True, True), (False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("T,H", LONG)
+def test_block_norm_backward_many_rows(T, H, rt, yt, post, nxt):
+    _backward_case(T, H, rt, yt, post, post, nxt, seed=T)
 
 
 @pytest.mark.parametrize("rt", [BF16, F32])
