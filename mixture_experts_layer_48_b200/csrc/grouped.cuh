@@ -109,23 +109,21 @@ MOE_DEVINL bool named_bar_and(int id, int nthreads, bool ok) {
       : "memory");
   return r != 0;
 }
-// sum[i] += column taddr + i of this warp's 32 TMEM lanes (lane = thread), 16 columns at a time so
+// sum[i] += column taddr + i of this warp's 32 TMEM lanes (lane = thread), 8 columns at a time so
 // that the loaded values need few registers beside the sums.
 MOE_DEVINL void tmem_add32(uint32_t taddr, float (&sum)[32]) {
 #pragma unroll
-  for (int h = 0; h < 32; h += 16) {
-    uint32_t r[16];
+  for (int h = 0; h < 32; h += 8) {
+    uint32_t r[8];
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15}, [%16];"
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-          "=r"(r[14]), "=r"(r[15])
+          "=r"(r[7])
         : "r"(taddr + h)
         : "memory");
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 16; ++i) sum[h + i] += __uint_as_float(r[i]);
+    for (int i = 0; i < 8; ++i) sum[h + i] += __uint_as_float(r[i]);
   }
 }
 // The two halves of cluster_sync_all, for whole warps.
@@ -606,6 +604,12 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
 
 // ------------------------------------------------------------------------------------------------
 // CTA pairs: 256 x 256 result tiles.  Shared by the many-row product and the weight gradient.
+//
+// The even CTA issues the MMAs, so it has to learn when both CTAs have read an accumulator.  Its own
+// epilogue threads arrive on acc_empty; the odd CTA's arrive on their CTA's `drained`, and that
+// CTA's otherwise idle MMA lane passes each completed phase on.  (An arrival across the cluster
+// releases at cluster scope, which waits for the arriving thread's global stores: from the
+// epilogue threads it cost 1.3 us a tile.)
 // ------------------------------------------------------------------------------------------------
 constexpr int kPairStages = 6;
 constexpr int kPairHalf = 128;                                 // rows and columns staged per CTA
@@ -641,13 +645,26 @@ MOE_DEVINL void pair_store(const uint32_t* w, uint32_t* stage, int lane, void* o
   __syncwarp();
 }
 
+// Odd CTA, one lane: passes the completed phases of `drained` for the accumulators unit ..
+// unit + pieces - 1 on to the even CTA's acc_empty.
+MOE_DEVINL bool pair_relay(int pieces, int& unit, uint64_t* drained, uint64_t* acc_empty,
+                           volatile int* abort_flag, uint32_t* status) {
+  for (int p = 0; p < pieces; ++p, ++unit) {
+    const int buf = unit & 1;
+    if (!wait_or_abort(&drained[buf], (unit >> 1) & 1u, abort_flag, status)) return false;
+    mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+  }
+  return true;
+}
+
 // The epilogue of one tile for one warp: 32 rows (TMEM lanes of its quarter) x 128 columns, from
 // `pieces` accumulators in turn.  taddr: this warp's lanes and first column in buffer 0.  unit: the
 // accumulators handed over so far.  rows_ok <= 0: nothing to write, the hand-over only.
-// pieces = 0 writes zeros.  Returns false when a wait gave up.
+// pieces = 0 writes zeros.  acc_read: this CTA's acc_empty or drained.  Returns false when a wait
+// gave up.
 template <bool F32>
 MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* acc_full,
-                              uint64_t* acc_empty, uint32_t* stage, int lane, void* out,
+                              uint64_t* acc_read, uint32_t* stage, int lane, void* out,
                               size_t row0, int rows_ok, int col0, int ld, volatile int* abort_flag,
                               uint32_t* status) {
   const bool mine = rows_ok > 0 && col0 < ld;   // warp-uniform
@@ -666,7 +683,7 @@ MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* a
         for (int c = 0; c < 4; ++c) tmem_add32(taddr + buf * 256 + 32 * c, sum[c]);
       }
       tc_fence_before();
-      mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+      mbar_arrive(&acc_read[buf]);
     }
     if (!mine) return true;
 #pragma unroll
@@ -700,7 +717,7 @@ MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* a
     }
     if (pieces > 0) {
       tc_fence_before();
-      mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+      mbar_arrive(&acc_read[buf]);
       ++unit;
     }
   }
@@ -725,7 +742,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   uint64_t* empty = full + kPairStages;
   uint64_t* acc_full = empty + kPairStages;
   uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* drained = acc_empty + 2;   // odd CTA: its epilogue has read the accumulator
+  uint64_t* drain = drained + 2;
   uint32_t* epi = reinterpret_cast<uint32_t*>(ring + kPairStages * kPairStageBytes + 256);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank();
@@ -742,7 +760,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 2 * 32 * kPairEpiWarps);
+      mbar_init(&acc_empty[b], 32 * kPairEpiWarps + 1);   // even CTA's threads, odd CTA's relay
+      mbar_init(&drained[b], 32 * kPairEpiWarps);
     }
     mbar_init(drain, 1);
     s_abort = 0;
@@ -872,17 +891,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         if (!mbar_wait_bounded(drain, 0, kWaitLimitNs)) atomicOr(a.status, kStatusTimeout);
       }
     }
+    if (!leader && lane == 0) {
+      const int pieces = (nk + piece - 1) / piece;
+      int unit = 0;
+      for (int t = pair; t < tiles; t += npairs)
+        if (!pair_relay(pieces, unit, drained, acc_empty, abort_flag, a.status)) break;
+    }
   } else {
     // ------------------------------ epilogue (both CTAs) ------------------------------
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + 128 * half;
     uint32_t* stage = epi + (warp - 2) * 32 * kPairEpiPitch;
+    uint64_t* acc_read = leader ? acc_empty : drained;
     const int pieces = (nk + piece - 1) / piece;
     const int r0 = rank * kPairHalf + 32 * q;   // this warp's first row of a tile
     int unit = 0;
     for (int t = pair; t < tiles; t += npairs) {
       const Tile w = tile_at(t);
-      if (!pair_epilogue<F32>(taddr, pieces, unit, acc_full, acc_empty, stage, lane, a.out,
+      if (!pair_epilogue<F32>(taddr, pieces, unit, acc_full, acc_read, stage, lane, a.out,
                               (size_t)w.row0 + r0, w.rows - r0, w.n0 + 128 * half, a.Ncols,
                               abort_flag, a.status))
         break;
@@ -894,6 +920,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_2sm(tmem_base, 512);
+}
+
+// Accumulators of one weight-gradient tile whose expert has cnt rows.
+template <bool F32>
+MOE_DEVINL int wgrad_pieces(int cnt) {
+  return F32 ? (cnt + kGrPieceStages * kGrBK - 1) / (kGrPieceStages * kGrBK) : cnt > 0;
 }
 
 // Weight gradient.  Tile: 256 x 256 of dW[e]; the reduction runs over e's rows, 64 per stage,
@@ -920,7 +952,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
   uint64_t* peer_masked = ragged + kPairStages;  // even CTA: the odd CTA has masked its part
   uint64_t* acc_full = peer_masked + kPairStages;
   uint64_t* acc_empty = acc_full + 2;
-  uint64_t* drain = acc_empty + 2;
+  uint64_t* drained = acc_empty + 2;   // odd CTA: its epilogue has read the accumulator
+  uint64_t* drain = drained + 2;
   uint32_t* epi = reinterpret_cast<uint32_t*>(ring + kPairStages * kPairStageBytes + 256);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = (int)cluster_ctarank();
@@ -939,7 +972,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
-      mbar_init(&acc_empty[b], 2 * 32 * kPairEpiWarps);
+      mbar_init(&acc_empty[b], 32 * kPairEpiWarps + 1);   // even CTA's threads, odd CTA's relay
+      mbar_init(&drained[b], 32 * kPairEpiWarps);
     }
     mbar_init(drain, 1);
     s_abort = 0;
@@ -1067,6 +1101,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         if (!mbar_wait_bounded(drain, 0, kWaitLimitNs)) atomicOr(a.status, kStatusTimeout);
       }
     }
+    if (!leader && lane == 0) {
+      int unit = 0;
+      for (int t = pair; t < tiles; t += npairs)
+        if (!pair_relay(wgrad_pieces<F32>(seg.cnt[t / per]), unit, drained, acc_empty, abort_flag,
+                        a.status))
+          break;
+    }
   } else if (warp == 2 + kPairEpiWarps) {
     // ------------------------------ masking of ragged ends (both CTAs) ------------------------
     uint32_t it = 0, ragged_ph = 0;
@@ -1100,13 +1141,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + 128 * half;
     uint32_t* stage = epi + (warp - 2) * 32 * kPairEpiPitch;
+    uint64_t* acc_read = leader ? acc_empty : drained;
     int unit = 0;
     for (int t = pair; t < tiles; t += npairs) {
       const int e = t / per, l = t - e * per;
       const int m0 = l / NT * 256 + rank * kPairHalf + 32 * q, n0 = l % NT * 256 + 128 * half;
       const int cnt = seg.cnt[e];
-      const int pieces = F32 ? (cnt + kGrPieceStages * kGrBK - 1) / (kGrPieceStages * kGrBK) : cnt > 0;
-      if (!pair_epilogue<F32>(taddr, pieces, unit, acc_full, acc_empty, stage, lane, a.out,
+      if (!pair_epilogue<F32>(taddr, wgrad_pieces<F32>(cnt), unit, acc_full, acc_read, stage, lane, a.out,
                               (size_t)e * a.M + m0, a.M - m0, n0, a.Ncols, abort_flag, a.status))
         break;
     }
