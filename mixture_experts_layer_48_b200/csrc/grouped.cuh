@@ -616,33 +616,40 @@ constexpr int kPairHalf = 128;                                 // rows and colum
 constexpr int kPairABytes = kPairHalf * kGrBK * 2;             // 16 KB
 constexpr int kPairStageBytes = 2 * kPairABytes;               // 32 KB per CTA
 constexpr int kPairEpiWarps = 8;                               // two per TMEM lane quarter
-constexpr int kPairEpiPitch = 20;                              // 32-bit words per staged row of 16
-constexpr int kPairEpiBytes = kPairEpiWarps * 32 * kPairEpiPitch * 4;
+constexpr int kPairEpiPitch = 36;                              // 32-bit words per staged row of 32
+constexpr int kPairEpiBytes = kPairEpiWarps * 16 * kPairEpiPitch * 4;
 constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 256 + kPairEpiBytes;
 constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
 constexpr int kWgradThreads = kPairThreads + 32;               // + the warp that masks ragged ends
 static_assert(kPairSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
 
-// One warp's 32 rows x 64 bytes (16 words w per lane, lane = row) to columns col0 .. of `out` (row
-// stride ld, first row row0), through shared memory so that four lanes write 64 contiguous bytes
-// of a row.  rows_ok: valid rows of the 32.
+// One warp's 32 rows x 128 bytes (32 words w per lane, lane = row) to columns col0 .. of `out` (row
+// stride ld, first row row0), 16 rows at a time through shared memory so that eight lanes write
+// one whole 128-byte line (64 bytes a row ran at half HBM's write rate).  rows_ok: valid rows of
+// the 32.
 template <bool F32>
 MOE_DEVINL void pair_store(const uint32_t* w, uint32_t* stage, int lane, void* out, size_t row0,
                            int rows_ok, int col0, int ld) {
-  uint4* mine = reinterpret_cast<uint4*>(stage + lane * kPairEpiPitch);
+  const int col = col0 + (lane & 7) * (F32 ? 4 : 8);
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    mine[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-  __syncwarp();
-  const int col = col0 + (lane & 3) * (F32 ? 4 : 8);
+  for (int h = 0; h < 2; ++h) {
+    if (lane >> 4 == h) {
+      uint4* mine = reinterpret_cast<uint4*>(stage + (lane & 15) * kPairEpiPitch);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = 8 * i + (lane >> 2);
-    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kPairEpiPitch + 4 * (lane & 3));
-    if (r < rows_ok && col < ld)
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) + ((row0 + r) * ld + col) * (F32 ? 4 : 2)) = v;
+      for (int i = 0; i < 8; ++i)
+        mine[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      const uint4 v = *reinterpret_cast<const uint4*>(stage + r * kPairEpiPitch + 4 * (lane & 7));
+      if (16 * h + r < rows_ok && col < ld)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(out) +
+                                  ((row0 + 16 * h + r) * ld + col) * (F32 ? 4 : 2)) = v;
+    }
+    __syncwarp();
   }
-  __syncwarp();
 }
 
 // Odd CTA, one lane: passes the completed phases of `drained` for the accumulators unit ..
@@ -687,11 +694,11 @@ MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* a
     }
     if (!mine) return true;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      uint32_t w[16];
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[32];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(sum[c / 2][16 * (c % 2) + i]);
-      pair_store<true>(w, stage, lane, out, row0, rows_ok, col0 + 16 * c, ld);
+      for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(sum[c][i]);
+      pair_store<true>(w, stage, lane, out, row0, rows_ok, col0 + 32 * c, ld);
     }
   } else {
     const int buf = unit & 1;
@@ -699,26 +706,29 @@ MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* a
       if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, status)) return false;
       tc_fence_after();
     }
-    if (mine) {
-#pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
-        if (pieces > 0) {
-          float v[32];
-          tmem_ld32(taddr + buf * 256 + 32 * c, v);
+    // all 128 columns into registers first: the accumulator is free while they are stored
+    uint32_t w[2][32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
-        } else {
+    for (int c = 0; c < 4; ++c) {
+      if (mine && pieces > 0) {
+        float v[32];
+        tmem_ld32(taddr + buf * 256 + 32 * c, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = 0u;
-        }
-        pair_store<false>(w, stage, lane, out, row0, rows_ok, col0 + 32 * c, ld);
+        for (int i = 0; i < 16; ++i) w[c / 2][16 * (c % 2) + i] = cvt_bf16x2(v[2 * i], v[2 * i + 1]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[c / 2][16 * (c % 2) + i] = 0u;
       }
     }
     if (pieces > 0) {
       tc_fence_before();
       mbar_arrive(&acc_read[buf]);
       ++unit;
+    }
+    if (mine) {
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        pair_store<false>(w[c], stage, lane, out, row0, rows_ok, col0 + 64 * c, ld);
     }
   }
   return true;
@@ -901,7 +911,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     // ------------------------------ epilogue (both CTAs) ------------------------------
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + 128 * half;
-    uint32_t* stage = epi + (warp - 2) * 32 * kPairEpiPitch;
+    uint32_t* stage = epi + (warp - 2) * 16 * kPairEpiPitch;
     uint64_t* acc_read = leader ? acc_empty : drained;
     const int pieces = (nk + piece - 1) / piece;
     const int r0 = rank * kPairHalf + 32 * q;   // this warp's first row of a tile
@@ -933,8 +943,8 @@ MOE_DEVINL int wgrad_pieces(int cnt) {
 // stage may hold rows of the next expert: a warp of each CTA overwrites them with zeros in both
 // operands (zeroing one would let a NaN or an infinity of the other through) before the MMAs
 // read them, up to the next multiple of 16; the MMAs stop there.  Such a stage's copies complete
-// on a barrier of their own CTA; the odd CTA's warp reports to the even one's, which completes the
-// stage's `full` phase.  (Ordinary stages take no arrival from the odd CTA: a release across the
+// on a barrier of their own CTA; then the even CTA's warp completes the stage's `full` phase and
+// the odd CTA's its `peer_masked` phase, and the MMA lane waits for both.  (Ordinary stages take no arrival from the odd CTA: a release across the
 // cluster in its producer lane cost 0.45 us a stage, half the kernel's rate.)
 // Experts without rows get zeros.
 template <bool F32>
@@ -1056,7 +1066,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
       const uint32_t ring_s = smem_u32(ring);
       const uint64_t adesc0 = smem_desc_sw128(ring_s, 64 * kGrBK * 2, 1024);
       const uint64_t bdesc0 = smem_desc_sw128(ring_s + kPairABytes, 64 * kGrBK * 2, 1024);
-      uint32_t it = 0;
+      uint32_t it = 0, masked_ph = 0;   // bit s: parity of the next masked stage in slot s
       int unit = 0;
       bool issued = false, ok = true;
       for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
@@ -1076,6 +1086,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
             if (!wait_or_abort(&full[slot], (it / kPairStages) & 1u, abort_flag, a.status)) {
               ok = false;
               break;
+            }
+            if (cnt - r < kGrBK) {
+              const uint32_t ph = (masked_ph >> slot) & 1u;
+              masked_ph ^= 1u << slot;
+              if (!wait_or_abort_cluster(&peer_masked[slot], ph, abort_flag, a.status)) {
+                ok = false;
+                break;
+              }
             }
             tc_fence_after();
             const uint64_t soff = (uint64_t)((slot * kPairStageBytes) >> 4);
@@ -1127,20 +1145,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         *reinterpret_cast<uint4*>(st + box * (64 * kGrBK * 2) + (rem + j / 8) * 128 + (j % 8) * 16) =
             make_uint4(0, 0, 0, 0);
       }
-      fence_proxy_async_smem();
+      if (pad > 0) fence_proxy_async_smem();
       __syncwarp();
-      if (!leader) {
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&peer_masked[slot]), 0));
-      } else {
-        if (!warp_wait_cluster(&peer_masked[slot], ph, abort_flag, a.status)) break;
-        if (lane == 0) mbar_arrive(&full[slot]);
+      if (lane == 0) {
+        if (leader) mbar_arrive(&full[slot]);
+        else mbar_arrive_cluster(mapa_shared(smem_u32(&peer_masked[slot]), 0));
       }
     }
   } else {
     // ------------------------------ epilogue (both CTAs) ------------------------------
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + 128 * half;
-    uint32_t* stage = epi + (warp - 2) * 32 * kPairEpiPitch;
+    uint32_t* stage = epi + (warp - 2) * 16 * kPairEpiPitch;
     uint64_t* acc_read = leader ? acc_empty : drained;
     int unit = 0;
     for (int t = pair; t < tiles; t += npairs) {
