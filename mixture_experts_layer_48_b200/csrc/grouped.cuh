@@ -620,7 +620,7 @@ constexpr int kPairEpiPitch = 36;                              // 32-bit words p
 constexpr int kPairEpiBytes = kPairEpiWarps * 16 * kPairEpiPitch * 4;
 constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 256 + kPairEpiBytes;
 constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
-constexpr int kWgradThreads = kPairThreads + 32;               // + the warp that masks ragged ends
+constexpr int kWgradThreads = kPairThreads + 64;   // + warps that mask ragged ends and report it
 static_assert(kPairSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
 
 // One warp's 32 rows x 128 bytes (32 words w per lane, lane = row) to columns col0 .. of `out` (row
@@ -943,9 +943,11 @@ MOE_DEVINL int wgrad_pieces(int cnt) {
 // stage may hold rows of the next expert: a warp of each CTA overwrites them with zeros in both
 // operands (zeroing one would let a NaN or an infinity of the other through) before the MMAs
 // read them, up to the next multiple of 16; the MMAs stop there.  Such a stage's copies complete
-// on a barrier of their own CTA; then the even CTA's warp completes the stage's `full` phase and
-// the odd CTA's its `peer_masked` phase, and the MMA lane waits for both.  (Ordinary stages take no arrival from the odd CTA: a release across the
-// cluster in its producer lane cost 0.45 us a stage, half the kernel's rate.)
+// on a barrier of their own CTA; then the even CTA's warp completes the stage's `full` phase, the
+// odd CTA's its `masked` phase, which a lane of a warp of its own passes on, and the MMA lane
+// waits for both.  No thread that writes memory arrives across the cluster, and ordinary stages take no
+// arrival from the odd CTA: the release waits for the thread's writes (0.45 us a stage from the
+// producer lane, half the kernel's rate; 0.5 us a tile from the masking warp).
 // Experts without rows get zeros.
 template <bool F32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
@@ -959,8 +961,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + kPairStages * kPairStageBytes);
   uint64_t* empty = full + kPairStages;
   uint64_t* ragged = empty + kPairStages;   // this CTA's copies of a stage that gets masked
-  uint64_t* peer_masked = ragged + kPairStages;  // even CTA: the odd CTA has masked its part
-  uint64_t* acc_full = peer_masked + kPairStages;
+  uint64_t* masked = ragged + kPairStages;       // odd CTA: it has masked its part of a stage
+  uint64_t* peer_masked = masked;                // even CTA: the odd CTA has
+  uint64_t* acc_full = masked + kPairStages;
   uint64_t* acc_empty = acc_full + 2;
   uint64_t* drained = acc_empty + 2;   // odd CTA: its epilogue has read the accumulator
   uint64_t* drain = drained + 2;
@@ -978,7 +981,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&ragged[s], 1);
-      mbar_init(&peer_masked[s], 1);
+      mbar_init(&masked[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -1147,9 +1150,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
       }
       if (pad > 0) fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        if (leader) mbar_arrive(&full[slot]);
-        else mbar_arrive_cluster(mapa_shared(smem_u32(&peer_masked[slot]), 0));
+      if (lane == 0) mbar_arrive(leader ? &full[slot] : &masked[slot]);
+    }
+  } else if (warp == 3 + kPairEpiWarps) {
+    // ------------------------------ masked stages reported (odd CTA) ------------------------------
+    if (!leader && lane == 0) {
+      uint32_t it = 0, masked_ph = 0;
+      for (int t = pair; t < tiles; t += npairs) {
+        const int cnt = seg.cnt[t / per];
+        it += (cnt + kGrBK - 1) / kGrBK;
+        if (cnt % kGrBK == 0) continue;
+        const int slot = (it - 1) % kPairStages;
+        if (!wait_or_abort(&masked[slot], (masked_ph >> slot) & 1u, abort_flag, a.status)) break;
+        masked_ph ^= 1u << slot;
+        mbar_arrive_cluster(mapa_shared(smem_u32(&peer_masked[slot]), 0));
       }
     }
   } else {
