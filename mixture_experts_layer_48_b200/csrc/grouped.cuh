@@ -622,6 +622,7 @@ constexpr int kPairSmem = 1024 + kPairStages * kPairStageBytes + 256 + kPairEpiB
 constexpr int kPairThreads = 64 + 32 * kPairEpiWarps;
 constexpr int kWgradThreads = kPairThreads + 64;   // + warps that mask ragged ends and report it
 static_assert(kPairSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
+static_assert(128 * 260 * 4 <= kPairStages * kPairStageBytes, "exchange of a split tile");
 
 // One warp's 32 rows x 128 bytes (32 words w per lane, lane = row) to columns col0 .. of `out` (row
 // stride ld, first row row0), 16 rows at a time through shared memory so that eight lanes write
@@ -653,13 +654,36 @@ MOE_DEVINL void pair_store(const uint32_t* w, uint32_t* stage, int lane, void* o
 }
 
 // Odd CTA, one lane: passes the completed phases of `drained` for the accumulators unit ..
-// unit + pieces - 1 on to the even CTA's acc_empty.
-MOE_DEVINL bool pair_relay(int pieces, int& unit, uint64_t* drained, uint64_t* acc_empty,
+// unit + pieces - 1 on to the acc_empty of the even CTA, number `even` of the cluster.
+MOE_DEVINL bool pair_relay(int pieces, int& unit, uint64_t* drained, uint64_t* acc_empty, int even,
                            volatile int* abort_flag, uint32_t* status) {
   for (int p = 0; p < pieces; ++p, ++unit) {
     const int buf = unit & 1;
     if (!wait_or_abort(&drained[buf], (unit >> 1) & 1u, abort_flag, status)) return false;
-    mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), 0));
+    mbar_arrive_cluster(mapa_shared(smem_u32(&acc_empty[buf]), even));
+  }
+  return true;
+}
+
+// Adds the `pieces` accumulators of a tile (32 rows x 128 columns of this warp) up in sum[][].
+// mine: whether this warp's part is wanted.  Returns false when a wait gave up.
+MOE_DEVINL bool pair_collect(uint32_t taddr, int pieces, int& unit, uint64_t* acc_full,
+                             uint64_t* acc_read, bool mine, float (&sum)[4][32],
+                             volatile int* abort_flag, uint32_t* status) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+#pragma unroll
+    for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
+  for (int p = 0; p < pieces; ++p, ++unit) {
+    const int buf = unit & 1;
+    if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, status)) return false;
+    tc_fence_after();
+    if (mine) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_add32(taddr + buf * 256 + 32 * c, sum[c]);
+    }
+    tc_fence_before();
+    mbar_arrive(&acc_read[buf]);
   }
   return true;
 }
@@ -677,21 +701,8 @@ MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* a
   const bool mine = rows_ok > 0 && col0 < ld;   // warp-uniform
   if constexpr (F32) {
     float sum[4][32];
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-      for (int i = 0; i < 32; ++i) sum[c][i] = 0.f;
-    for (int p = 0; p < pieces; ++p, ++unit) {
-      const int buf = unit & 1;
-      if (!warp_wait(&acc_full[buf], (unit >> 1) & 1u, abort_flag, status)) return false;
-      tc_fence_after();
-      if (mine) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_add32(taddr + buf * 256 + 32 * c, sum[c]);
-      }
-      tc_fence_before();
-      mbar_arrive(&acc_read[buf]);
-    }
+    if (!pair_collect(taddr, pieces, unit, acc_full, acc_read, mine, sum, abort_flag, status))
+      return false;
     if (!mine) return true;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -905,7 +916,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int pieces = (nk + piece - 1) / piece;
       int unit = 0;
       for (int t = pair; t < tiles; t += npairs)
-        if (!pair_relay(pieces, unit, drained, acc_empty, abort_flag, a.status)) break;
+        if (!pair_relay(pieces, unit, drained, acc_empty, 0, abort_flag, a.status)) break;
     }
   } else {
     // ------------------------------ epilogue (both CTAs) ------------------------------
@@ -949,10 +960,16 @@ MOE_DEVINL int wgrad_pieces(int cnt) {
 // arrival from the odd CTA: the release waits for the thread's writes (0.45 us a stage from the
 // producer lane, half the kernel's rate; 0.5 us a tile from the masking warp).
 // Experts without rows get zeros.
-template <bool F32>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
+//
+// SPLIT: where the tiles are too few for the GPU, a cluster of `pairs` (2 or 4) CTA pairs takes one
+// tile, each pair a run of the segment's stages.  Afterwards every CTA holds partial sums of its
+// 128 rows of the tile; CTA (pair p, half h) gets those of its 128 / pairs rows from the other
+// pairs' CTAs of half h through distributed shared memory (the rings, idle by then), adds them in
+// pair order and writes them.
+template <bool F32, bool SPLIT>
+__global__ void __launch_bounds__(kWgradThreads, 1)
     grouped_wgrad_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap xmap,
-                         const __grid_constant__ CUtensorMap dymap) {
+                         const __grid_constant__ CUtensorMap dymap, const int pairs) {
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __shared__ Segments seg;
   __shared__ uint32_t s_tmem;
@@ -969,7 +986,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
   uint64_t* drain = drained + 2;
   uint32_t* epi = reinterpret_cast<uint32_t*>(ring + kPairStages * kPairStageBytes + 256);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = (int)cluster_ctarank();
+  const int cta = (int)cluster_ctarank();
+  const int rank = cta & 1, even = cta & ~1;   // half of the pair, its even CTA
   const bool leader = rank == 0;
 
   if (warp == 1) {
@@ -1005,8 +1023,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
 
   const int NT = (a.Ncols + 255) / 256, MT = (a.M + 255) / 256;
   const int per = NT * MT, tiles = a.E * per;
-  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  // SPLIT: one tile per cluster; else the pairs walk the tiles
+  const int pair = SPLIT ? (int)blockIdx.x / (2 * pairs) : (int)blockIdx.x >> 1;
+  const int npairs = SPLIT ? tiles : (int)gridDim.x >> 1;
   volatile int* abort_flag = &s_abort;
+  // This pair's rows [r0, r1) of an expert's cnt.
+  struct Range { int r0, r1; };
+  auto range_of = [&](int cnt) {
+    if (!SPLIT) return Range{0, cnt};
+    const long long stages = (cnt + kGrBK - 1) / kGrBK;
+    const int p = cta >> 1;
+    return Range{min(cnt, (int)(stages * p / pairs) * kGrBK),
+                 min(cnt, (int)(stages * (p + 1) / pairs) * kGrBK)};
+  };
 
   if (warp == 0) {
     // ------------------------------ TMA producer (both CTAs) ------------------------------
@@ -1020,8 +1049,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
         const int e = t / per, l = t - e * per;
         const int m0 = l / NT * 256 + rank * kPairHalf, n0 = l % NT * 256 + rank * kPairHalf;
         const int beg = seg.beg[e], cnt = seg.cnt[e];
+        const Range rg = range_of(cnt);
         bool ok = true;
-        for (int r = 0; r < cnt; r += kGrBK, ++it) {
+        for (int r = rg.r0; r < rg.r1; r += kGrBK, ++it) {
           const int slot = it % kPairStages;
           if (!wait_or_abort(&empty[slot], ((it / kPairStages) & 1u) ^ 1u, abort_flag, a.status)) {
             ok = false;
@@ -1030,7 +1060,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
           uint8_t* st = ring + slot * kPairStageBytes;
           constexpr int kBox = 64 * kGrBK * 2;
           if (cnt - r >= kGrBK) {
-            const uint32_t bar = mapa_shared(smem_u32(&full[slot]), 0);
+            const uint32_t bar = mapa_shared(smem_u32(&full[slot]), even);
             if (leader) mbar_arrive_expect_tx(&full[slot], 2 * kPairStageBytes);
             tma_load_2d_pair(st, &xmap, m0, beg + r, bar);
             tma_load_2d_pair(st + kBox, &xmap, m0 + 64, beg + r, bar);
@@ -1074,9 +1104,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
       bool issued = false, ok = true;
       for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
         const int cnt = seg.cnt[t / per];
+        const Range rg = range_of(cnt);
         const int piece = F32 ? kGrPieceStages * kGrBK : max(cnt, 1);
-        for (int p0 = 0; ok && p0 < cnt; p0 += piece, ++unit) {
-          const int p1 = min(cnt, p0 + piece);
+        for (int p0 = rg.r0; ok && p0 < rg.r1; p0 += piece, ++unit) {
+          const int p1 = min(rg.r1, p0 + piece);
           const int buf = unit & 1;
           if (!wait_or_abort(&acc_empty[buf], ((unit >> 1) & 1u) ^ 1u, abort_flag, a.status)) {
             ok = false;
@@ -1107,13 +1138,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
                               bdesc0 + soff + ((k16 * 2048) >> 4), idesc, r != p0 || k16 != 0);
             const uint32_t e_local = smem_u32(&empty[slot]);
             tc_commit_2sm(e_local);
-            tc_commit_2sm(mapa_shared(e_local, 1));
+            tc_commit_2sm(mapa_shared(e_local, even + 1));
             issued = true;
           }
           if (ok) {
             const uint32_t f_local = smem_u32(&acc_full[buf]);
             tc_commit_2sm(f_local);
-            tc_commit_2sm(mapa_shared(f_local, 1));
+            tc_commit_2sm(mapa_shared(f_local, even + 1));
           }
         }
       }
@@ -1124,18 +1155,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     }
     if (!leader && lane == 0) {
       int unit = 0;
-      for (int t = pair; t < tiles; t += npairs)
-        if (!pair_relay(wgrad_pieces<F32>(seg.cnt[t / per]), unit, drained, acc_empty, abort_flag,
+      for (int t = pair; t < tiles; t += npairs) {
+        const Range rg = range_of(seg.cnt[t / per]);
+        if (!pair_relay(wgrad_pieces<F32>(rg.r1 - rg.r0), unit, drained, acc_empty, even, abort_flag,
                         a.status))
           break;
+      }
     }
   } else if (warp == 2 + kPairEpiWarps) {
     // ------------------------------ masking of ragged ends (both CTAs) ------------------------
     uint32_t it = 0, ragged_ph = 0;
     for (int t = pair; t < tiles; t += npairs) {
-      const int cnt = seg.cnt[t / per], stages = (cnt + kGrBK - 1) / kGrBK, rem = cnt % kGrBK;
-      it += stages;
-      if (rem == 0) continue;
+      const Range rg = range_of(seg.cnt[t / per]);   // r0 is a multiple of a stage
+      const int rem = rg.r1 % kGrBK;
+      it += (rg.r1 - rg.r0 + kGrBK - 1) / kGrBK;
+      if (rg.r1 == rg.r0 || rem == 0) continue;
       const int slot = (it - 1) % kPairStages;
       const uint32_t ph = (ragged_ph >> slot) & 1u;
       ragged_ph ^= 1u << slot;
@@ -1157,16 +1191,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     if (!leader && lane == 0) {
       uint32_t it = 0, masked_ph = 0;
       for (int t = pair; t < tiles; t += npairs) {
-        const int cnt = seg.cnt[t / per];
-        it += (cnt + kGrBK - 1) / kGrBK;
-        if (cnt % kGrBK == 0) continue;
+        const Range rg = range_of(seg.cnt[t / per]);
+        it += (rg.r1 - rg.r0 + kGrBK - 1) / kGrBK;
+        if (rg.r1 == rg.r0 || rg.r1 % kGrBK == 0) continue;
         const int slot = (it - 1) % kPairStages;
         if (!wait_or_abort(&masked[slot], (masked_ph >> slot) & 1u, abort_flag, a.status)) break;
         masked_ph ^= 1u << slot;
-        mbar_arrive_cluster(mapa_shared(smem_u32(&peer_masked[slot]), 0));
+        mbar_arrive_cluster(mapa_shared(smem_u32(&peer_masked[slot]), even));
       }
     }
-  } else {
+  } else if (!SPLIT) {
     // ------------------------------ epilogue (both CTAs) ------------------------------
     const int q = warp & 3, half = (warp - 2) >> 2;
     const uint32_t taddr = tmem_base + ((uint32_t)(32 * q) << 16) + 128 * half;
@@ -1183,6 +1217,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWgradThreads, 1)
     }
   }
 
+  if constexpr (SPLIT) {
+    // ------------------------------ exchange (tile `pair`, every warp) ------------------------
+    const bool epi_warp = warp >= 2 && warp < 2 + kPairEpiWarps;
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    const int e = pair / per, l = pair - e * per;
+    const int m0 = l / NT * 256 + rank * kPairHalf, n0 = l % NT * 256;
+    const int share = kPairHalf / pairs;           // rows of the tile that this CTA writes
+    constexpr int kPitch = 260;                    // floats per row of 256 in the exchange
+    float sum[4][32];
+    if (epi_warp) {
+      const Range rg = range_of(seg.cnt[e]);
+      int unit = 0;
+      pair_collect(tmem_base + ((uint32_t)(32 * q) << 16) + 128 * half,
+                   wgrad_pieces<F32>(rg.r1 - rg.r0), unit, acc_full, leader ? acc_empty : drained,
+                   true, sum, abort_flag, a.status);
+    }
+    __syncwarp();
+    cluster_sync_all();   // no CTA of the cluster has copies or MMAs on its ring any more
+    if (epi_warp) {
+      const int row = 32 * q + lane;
+      const uint32_t to = mapa_shared(
+          smem_u32(ring) + 4u * (((cta >> 1) * share + row % share) * kPitch + 128 * half),
+          2 * (row / share) + rank);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+          asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           to + 4 * (32 * c + i)),
+                       "f"(sum[c][i]), "f"(sum[c][i + 1]), "f"(sum[c][i + 2]), "f"(sum[c][i + 3])
+                       : "memory");
+    }
+    __syncwarp();
+    cluster_sync_all();   // every CTA has the sums of its rows
+    if (epi_warp) {
+      const float* part = reinterpret_cast<const float*>(ring);
+      const int row0 = m0 + (cta >> 1) * share;
+      for (int i = tid - 64; i < share * 64; i += 32 * kPairEpiWarps) {
+        const int r = i / 64, c4 = 4 * (i % 64);
+        if (row0 + r >= a.M || n0 + c4 >= a.Ncols) continue;
+        float4 v = *reinterpret_cast<const float4*>(part + r * kPitch + c4);
+        for (int p = 1; p < pairs; ++p) {
+          const float4 o = *reinterpret_cast<const float4*>(part + (p * share + r) * kPitch + c4);
+          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
+        store4<F32>(a.out, ((size_t)e * a.M + row0 + r) * a.Ncols + n0 + c4, v);
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();

@@ -93,8 +93,8 @@ struct moe_ctx {
   uint32_t* d_status = nullptr;
   cudaStream_t aux = nullptr;            // second stream for a call whose families fork
   cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
-  // clusters of 2 and 4 one-CTA-per-SM blocks that run at the same time (grouped products)
-  int max_clusters[2] = {0, 0};
+  // clusters of 2, 4 and 8 one-CTA-per-SM blocks that run at the same time (grouped products)
+  int max_clusters[3] = {0, 0, 0};
   void* static_scratch = nullptr;  // device address of the routing scratch array (moe_route_static)
   uint64_t launches = 0;
   // profiling

@@ -78,10 +78,10 @@ bool set_grouped_attrs() {
          smem_attr(grouped_rows_kernel<TRANS, F32>, kPairSmem);
 }
 
-// Clusters of 2 and 4 CTAs of the few-row kernel (one CTA per SM) that fit the GPU at once: a
+// Clusters of 2, 4 and 8 CTAs of the few-row kernel (one CTA per SM) that fit the GPU at once: a
 // cluster lies inside one GPC, whose SM count need not be a multiple of its size.
 bool query_clusters(int num_sms, int* out) {
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 3; ++i) {
     const int size = 2 << i;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(num_sms / size * size);
@@ -157,6 +157,23 @@ GroupedPlan plan_grouped(const moe_ctx* c, int R, int Kred, int Ncols) {
                           s * 16384.0 / chunks(kColsSmallRows),
                           0.3 + 0.03 * std::min(mean, kColsSmallRows) + (s > 1 ? 0.4 : 0.0)));
     }
+  return best;
+}
+
+// CTA pairs that share a weight-gradient tile: 1 while the tiles fill the GPU or the segments are
+// short.  A stage of 64 rows takes about 0.42 us; an exchange about 4.
+int plan_wgrad(const moe_ctx* c, int R, int K, int N) {
+  const long long tiles = (long long)c->E * ((K + 255) / 256) * ((N + 255) / 256);
+  const double stages = std::max(1.0, (double)R / c->E / kGrBK);
+  int best = 1;
+  double us = grouped_us(tiles, c->num_sms / 2, stages, 0.42, 0.0, 0.0);
+  for (int pairs = 2; pairs <= 4; pairs *= 2) {
+    const double t = grouped_us(tiles, c->max_clusters[pairs / 2], stages / pairs, 0.42, 0.0, 4.0);
+    if (t < us) {
+      us = t;
+      best = pairs;
+    }
+  }
   return best;
 }
 
@@ -304,8 +321,10 @@ bool set_row_attrs() {
 bool set_rows_smem_attrs() {
   return set_grouped_attrs<false, false>() && set_grouped_attrs<false, true>() &&
          set_grouped_attrs<true, false>() && set_grouped_attrs<true, true>() &&
-         smem_attr(grouped_wgrad_kernel<false>, kPairSmem) &&
-         smem_attr(grouped_wgrad_kernel<true>, kPairSmem) && set_row_attrs();
+         smem_attr(grouped_wgrad_kernel<false, false>, kPairSmem) &&
+         smem_attr(grouped_wgrad_kernel<true, false>, kPairSmem) &&
+         smem_attr(grouped_wgrad_kernel<false, true>, kPairSmem) &&
+         smem_attr(grouped_wgrad_kernel<true, true>, kPairSmem) && set_row_attrs();
 }
 
 }  // namespace
@@ -359,10 +378,15 @@ moe_status moe_grouped_wgrad(moe_t c, int R, int K, int N, const int32_t* offset
   CUtensorMap xmap, dymap;
   if (!encode_rows(&xmap, x_rows_bf16, R, K, kGrBK) || !encode_rows(&dymap, dy_rows_bf16, R, N, kGrBK))
     return MOE_ERR_CUDA;
+  const bool f32 = out_type == MOE_F32;
+  const int pairs = plan_wgrad(c, R, K, N);
+  const int tiles = c->E * ((K + 255) / 256) * ((N + 255) / 256);
+  const int grid = pairs > 1 ? tiles * 2 * pairs : c->num_sms / 2 * 2;
+  auto kernel = pairs > 1 ? (f32 ? grouped_wgrad_kernel<true, true> : grouped_wgrad_kernel<false, true>)
+                          : (f32 ? grouped_wgrad_kernel<true, false> : grouped_wgrad_kernel<false, false>);
   return launch(c, -1, st, [&] {
-    return launch_pdl(out_type == MOE_F32 ? grouped_wgrad_kernel<true> : grouped_wgrad_kernel<false>,
-                      dim3(c->num_sms / 2 * 2), dim3(kWgradThreads), (size_t)kPairSmem, st, a, xmap,
-                      dymap);
+    return launch_pdl_cluster(kernel, dim3(grid), dim3(kWgradThreads), (size_t)kPairSmem, 2 * pairs,
+                              st, a, xmap, dymap, pairs);
   });
 }
 

@@ -149,6 +149,11 @@ def test_wgrad(counts, K, N, out_dtype):
     ([20000, 3], 128, 256, F32),                 # a long reduction, in pieces
     ([6144, 6145, 6143, 6208], 256, 256, F32),   # around the length of a piece
     ([63, 64, 65, 448, 449, 447, 0, 1, 1, 1, 2, 1], 256, 512, F32),
+    ([5000], 520, 264, BF16),                    # few tiles: the rows split over four CTA pairs
+    ([4097, 0, 70], 304, 72, F32),
+    ([2600], 64, 64, F32),
+    ([9001, 2], 1000, 1000, BF16),               # over two
+    ([100], 264, 2000, F32),
 ])
 def test_wgrad_sizes(counts, K, N, out_dtype):
     _wgrad_case(counts, K, N, out_dtype, seed=3)
