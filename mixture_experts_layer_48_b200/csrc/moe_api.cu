@@ -51,8 +51,6 @@ constexpr int kMxStreamT = 176;
 constexpr int kMaxKernelsPerCall = 12;
 
 moe_status static_scratch_address(void** out);  // defined beside the array, at the end
-bool set_rows_smem_attrs();                     // rows_api.cuh
-bool query_clusters(int num_sms, int* out);     // rows_api.cuh
 
 // Profiled kernel kinds (moe_profile_end): one per kernel family and projection.
 enum Kind { kKindRouter = 0, kKindRouteFin = 1, kKindGather = 2, kKindGateUp = 3,
@@ -95,6 +93,10 @@ struct moe_ctx {
   cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
   // clusters of 2, 4 and 8 one-CTA-per-SM blocks that run at the same time (grouped products)
   int max_clusters[3] = {0, 0, 0};
+  // kernels of rows_api.cuh whose shared-memory limit is set on this device
+  static constexpr int kMaxReady = 64;
+  const void* ready[kMaxReady];
+  int n_ready = 0;
   void* static_scratch = nullptr;  // device address of the routing scratch array (moe_route_static)
   uint64_t launches = 0;
   // profiling
@@ -642,7 +644,6 @@ bool set_smem_attrs() {
   ok &= cudaFuncSetAttribute(build_segment_lists_kernel,
                              cudaFuncAttributeMaxDynamicSharedMemorySize,
                              (4 * kMaxSegments + 2 * kMaxE) * 4) == cudaSuccess;
-  ok &= set_rows_smem_attrs();
   return ok;
 }
 
@@ -1057,11 +1058,6 @@ moe_status moe_create(int E, int H, int I, int k, moe_t* out) {
   c->device = dev;
   c->num_sms = prop.multiProcessorCount;
   c->stream_T = default_stream_T(c);
-  if (!query_clusters(c->num_sms, c->max_clusters)) {
-    cudaGetLastError();
-    delete c;
-    return MOE_ERR_CUDA;
-  }
   // row-tile width of the grouped GEMM: MOE_ROW_TILE=512 or 256 (default below)
   if (const char* v = getenv("MOE_ROW_TILE")) c->wide_rows = strcmp(v, "512") == 0;
   // rows per expert tile: MOE_TILE_ROWS=128 or 256 (default: by each call's mean load)

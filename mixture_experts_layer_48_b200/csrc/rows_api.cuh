@@ -64,29 +64,33 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
-template <typename K>
-bool smem_attr(K kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
-         cudaSuccess;
-}
-
-template <bool TRANS, bool F32>
-bool set_grouped_attrs() {
-  return smem_attr(grouped_cols_kernel<kColsSmallRows, 1, TRANS, F32>,
-                   ColsCfg<kColsSmallRows, 1>::kSmem) &&
-         smem_attr(grouped_cols_kernel<kColsRows, 2, TRANS, F32>, ColsCfg<kColsRows, 2>::kSmem) &&
-         smem_attr(grouped_rows_kernel<TRANS, F32>, kPairSmem);
+// Whether the kernel may take `bytes` of dynamic shared memory on the handle's device: asked for at
+// the handle's first use of the kernel (for all of them in moe_create it took 0.3 s of loading).
+template <typename... A>
+bool ready(moe_ctx* c, void (*kernel)(A...), size_t bytes) {
+  const void* f = reinterpret_cast<const void*>(kernel);
+  for (int i = 0; i < c->n_ready; ++i)
+    if (c->ready[i] == f) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+    return false;
+  if (c->n_ready < moe_ctx::kMaxReady) c->ready[c->n_ready++] = f;
+  return true;
 }
 
 // Clusters of 2, 4 and 8 CTAs of the few-row kernel (one CTA per SM) that fit the GPU at once: a
 // cluster lies inside one GPC, whose SM count need not be a multiple of its size.
-bool query_clusters(int num_sms, int* out) {
+bool query_clusters(moe_ctx* c) {
+  if (c->max_clusters[0] > 0) return true;
+  auto kernel = grouped_cols_kernel<kColsSmallRows, 1, false, false>;
+  const size_t smem = ColsCfg<kColsSmallRows, 1>::kSmem;
+  int out[3];
+  if (!ready(c, kernel, smem)) return false;
   for (int i = 0; i < 3; ++i) {
     const int size = 2 << i;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms / size * size);
+    cfg.gridDim = dim3(c->num_sms / size * size);
     cfg.blockDim = dim3(ColsCfg<kColsSmallRows, 1>::kThreads);
-    cfg.dynamicSmemBytes = ColsCfg<kColsSmallRows, 1>::kSmem;
+    cfg.dynamicSmemBytes = smem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = size;
@@ -94,11 +98,10 @@ bool query_clusters(int num_sms, int* out) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&out[i], grouped_cols_kernel<kColsSmallRows, 1, false, false>,
-                                       &cfg) != cudaSuccess ||
-        out[i] < 1)
+    if (cudaOccupancyMaxActiveClusters(&out[i], kernel, &cfg) != cudaSuccess || out[i] < 1)
       return false;
   }
+  for (int i = 0; i < 3; ++i) c->max_clusters[i] = out[i];
   return true;
 }
 
@@ -178,10 +181,11 @@ int plan_wgrad(const moe_ctx* c, int R, int K, int N) {
 }
 
 template <int ROWS, int NM, bool TRANS, bool F32>
-cudaError_t launch_cols(const moe_ctx* c, int split, const GroupedArgs& a, const CUtensorMap& wmap,
+cudaError_t launch_cols(moe_ctx* c, int split, const GroupedArgs& a, const CUtensorMap& wmap,
                         const CUtensorMap& xmap, cudaStream_t st) {
   auto kernel = grouped_cols_kernel<ROWS, NM, TRANS, F32>;
   const size_t smem = ColsCfg<ROWS, NM>::kSmem;
+  if (!ready(c, kernel, smem)) return cudaErrorInvalidConfiguration;
   const int clusters = split == 1 ? c->num_sms : c->max_clusters[split / 4];  // 2, 4 -> 0, 1
   return launch_pdl_cluster(kernel, dim3(clusters * split), dim3(ColsCfg<ROWS, NM>::kThreads), smem, split, st, a,
                             wmap, xmap, split);
@@ -190,6 +194,10 @@ cudaError_t launch_cols(const moe_ctx* c, int split, const GroupedArgs& a, const
 template <bool TRANS, bool F32>
 moe_status run_grouped(moe_ctx* c, const GroupedArgs& a, const void* W, const void* x, int K, int N,
                        cudaStream_t st) {
+  if (!query_clusters(c)) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
   const GroupedPlan p = plan_grouped(c, a.R, a.Kred, a.Ncols);
   const uint32_t box = p.kind == GroupedPlan::kRows       ? kPairHalf
                        : p.kind == GroupedPlan::kColsWide ? ColsCfg<kColsRows, 2>::kRowBox
@@ -206,6 +214,7 @@ moe_status run_grouped(moe_ctx* c, const GroupedArgs& a, const void* W, const vo
       case GroupedPlan::kColsWide:
         return launch_cols<kColsRows, 2, TRANS, F32>(c, p.split, a, wmap, xmap, st);
       default:
+        if (!ready(c, grouped_rows_kernel<TRANS, F32>, kPairSmem)) return cudaErrorInvalidConfiguration;
         return launch_pdl(grouped_rows_kernel<TRANS, F32>, dim3(c->num_sms / 2 * 2),
                           dim3(kPairThreads), (size_t)kPairSmem, st, a, wmap, xmap);
     }
@@ -294,39 +303,6 @@ int norm_backward_parts(const moe_ctx* c, int T) {
 template <int VPT>
 constexpr bool norm_staged() { return VPT <= 4; }
 
-bool set_row_attrs() {
-  for (int n4 = 16; n4 <= kMaxHI / 4; n4 += 16)
-    for (moe_dtype r : {MOE_BF16, MOE_F32})
-      for (moe_dtype y : {MOE_BF16, MOE_F32}) {
-        static_assert(kMaxHI % 64 == 0, "");
-        const moe_status s = by_row_length(n4, [&](auto tpr, auto vpt) {
-          constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
-          if (!norm_staged<VPT>() || n4 != TPR * VPT) return MOE_OK;   // each variant once
-          return by_types(r, y, [&](auto rt, auto yt) {
-            return smem_attr(block_norm_backward_kernel<TPR, VPT, decltype(rt), decltype(yt),
-                                                        norm_staged<VPT>()>,
-                             kRowRingBytes) &&
-                           smem_attr(block_norm_kernel<TPR, VPT, decltype(rt), decltype(yt),
-                                                       norm_staged<VPT>()>,
-                                     kRowRingBytes)
-                       ? MOE_OK
-                       : MOE_ERR_CUDA;
-          });
-        });
-        if (s != MOE_OK) return false;
-      }
-  return true;
-}
-
-bool set_rows_smem_attrs() {
-  return set_grouped_attrs<false, false>() && set_grouped_attrs<false, true>() &&
-         set_grouped_attrs<true, false>() && set_grouped_attrs<true, true>() &&
-         smem_attr(grouped_wgrad_kernel<false, false>, kPairSmem) &&
-         smem_attr(grouped_wgrad_kernel<true, false>, kPairSmem) &&
-         smem_attr(grouped_wgrad_kernel<false, true>, kPairSmem) &&
-         smem_attr(grouped_wgrad_kernel<true, true>, kPairSmem) && set_row_attrs();
-}
-
 }  // namespace
 
 extern "C" {
@@ -378,6 +354,10 @@ moe_status moe_grouped_wgrad(moe_t c, int R, int K, int N, const int32_t* offset
   CUtensorMap xmap, dymap;
   if (!encode_rows(&xmap, x_rows_bf16, R, K, kGrBK) || !encode_rows(&dymap, dy_rows_bf16, R, N, kGrBK))
     return MOE_ERR_CUDA;
+  if (!query_clusters(c)) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
   const bool f32 = out_type == MOE_F32;
   const int pairs = plan_wgrad(c, R, K, N);
   const int tiles = c->E * ((K + 255) / 256) * ((N + 255) / 256);
@@ -385,6 +365,7 @@ moe_status moe_grouped_wgrad(moe_t c, int R, int K, int N, const int32_t* offset
   auto kernel = pairs > 1 ? (f32 ? grouped_wgrad_kernel<true, true> : grouped_wgrad_kernel<false, true>)
                           : (f32 ? grouped_wgrad_kernel<true, false> : grouped_wgrad_kernel<false, false>);
   return launch(c, -1, st, [&] {
+    if (!ready(c, kernel, kPairSmem)) return cudaErrorInvalidConfiguration;
     return launch_pdl_cluster(kernel, dim3(grid), dim3(kWgradThreads), (size_t)kPairSmem, 2 * pairs,
                               st, a, xmap, dymap, pairs);
   });
@@ -468,8 +449,9 @@ moe_status moe_block_norm(moe_t c, int T, moe_dtype resid_type, moe_dtype y_type
         const RowPlan p = plan_rows(a.stage_bytes, norm_forward_blocks<TPR, VPT>());
         a.stages = p.stages;
         return launch(c, -1, st, [&] {
-          return launch_pdl(block_norm_kernel<TPR, VPT, RT, YT, norm_staged<VPT>()>,
-                            dim3(row_grid<TPR, VPT>(c, T, p.blocks)),
+          auto kernel = block_norm_kernel<TPR, VPT, RT, YT, norm_staged<VPT>()>;
+          if (!ready(c, kernel, kRowRingBytes)) return cudaErrorInvalidConfiguration;
+          return launch_pdl(kernel, dim3(row_grid<TPR, VPT>(c, T, p.blocks)),
                             dim3(RowCfg<TPR, VPT>::kThreads), (size_t)a.stages * a.stage_bytes, st,
                             a);
         });
@@ -555,8 +537,9 @@ moe_status moe_block_norm_backward(moe_t c, int T, moe_dtype resid_type, moe_dty
         const int grid = row_grid<TPR, VPT>(c, T, p.blocks);
         parts = grid * C::kRows;
         return launch(c, -1, st, [&] {
-          return launch_pdl(block_norm_backward_kernel<TPR, VPT, RT, YT, norm_staged<VPT>()>,
-                            dim3(grid), dim3(C::kThreads), (size_t)a.stages * a.stage_bytes, st, a);
+          auto kernel = block_norm_backward_kernel<TPR, VPT, RT, YT, norm_staged<VPT>()>;
+          if (a.stages && !ready(c, kernel, kRowRingBytes)) return cudaErrorInvalidConfiguration;
+          return launch_pdl(kernel, dim3(grid), dim3(C::kThreads), (size_t)a.stages * a.stage_bytes, st, a);
         });
       });
     }));
