@@ -159,6 +159,36 @@ def test_wgrad_sizes(counts, K, N, out_dtype):
     _wgrad_case(counts, K, N, out_dtype, seed=3)
 
 
+@pytest.mark.parametrize("K,N", [(32768, 8), (8, 32768), (32768, 72), (136, 32768)])
+def test_longest_rows(K, N):
+    for transpose in (False, True):
+        _matmul_case([3, 0, 130], K, N, transpose, BF16, seed=4)
+    _matmul_case([3, 0, 130], K, N, False, F32, seed=5)
+    _wgrad_case([3, 0, 130], K, N, BF16, seed=6)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_256_experts(rows):
+    counts = [rows if i % 3 else 0 for i in range(256)]
+    _matmul_case(counts, 128, 136, True, F32, first=2, tail=1, seed=7)
+    _wgrad_case(counts, 136, 64, BF16, first=2, tail=1, seed=8)
+
+
+def test_results_past_2_to_the_31_elements():
+    R, K, N = 70001, 8, 32768
+    g = _gen(9)
+    x, W = _normal(g, R, K), _normal(g, 2, K, N)
+    offsets = torch.tensor([0, 35000, R], dtype=torch.int32, device="cuda")
+    layer = moe.Moe(2, 64, 64, 1)
+    out = layer.grouped_matmul(x, W, offsets)
+    for r in (0, 34999, 35000, 65535, 65536, 66000, R - 1):
+        w = W[int(r >= 35000)].double()
+        _check(out[r:r + 1], x[r:r + 1].double() @ w, x[r:r + 1].double().abs() @ w.abs(), K, f"row {r}")
+    dW = layer.grouped_wgrad(x, out, offsets, out_dtype=F32)   # reads dy past 2^31 elements too
+    a, b = x[35000:].double(), out[35000:, -64:].double()
+    _check(dW[1][:, -64:], a.t() @ b, a.abs().t() @ b.abs(), 6144, "dW")
+
+
 def test_wgrad_rows_outside_the_segments():
     _wgrad_case(COUNTS["many"], 136, 152, BF16, first=5, tail=9)
     _wgrad_case(COUNTS["few"], 136, 152, F32, first=70, tail=70)
@@ -251,6 +281,27 @@ def test_captured_and_on_another_stream():
     assert torch.equal(out, layer.grouped_matmul(x, W, offsets2))
     assert torch.equal(dWg, layer.grouped_wgrad(x, out, offsets2, out_dtype=F32))
     assert layer.sync_status() == moe.MOE_OK
+
+
+def test_calls_side_by_side():
+    """Kernels of every shape on four streams at once, each with its own handle."""
+    g = _gen(10)
+    work = []
+    for i, counts in enumerate(["few", "mid", "many", "one expert long"]):
+        o, offsets = _offsets(COUNTS[counts])
+        E = len(COUNTS[counts])
+        work.append((moe.Moe(E, 64, 64, 1), _normal(g, o[-1], 520), _normal(g, E, 520, 264), offsets, torch.cuda.Stream()))
+    want = [(h.grouped_matmul(x, W, o), h.grouped_wgrad(x, x, o, out_dtype=F32)) for h, x, W, o, _ in work]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got.append([(h.grouped_matmul(x, W, o, stream=s), h.grouped_wgrad(x, x, o, out_dtype=F32, stream=s))
+                    for h, x, W, o, s in work])
+    torch.cuda.synchronize()
+    for run in got:
+        for (y, dW), (yw, dWw) in zip(run, want):
+            assert torch.equal(y, yw) and torch.equal(dW, dWw)
+    assert all(h.sync_status() == moe.MOE_OK for h, *_ in work)
 
 
 def test_gradients_are_those_of_the_product():

@@ -78,6 +78,23 @@ def test_swiglu_large_gates():
     _swiglu_case(40, 256, True, seed=5, std=3e3)
 
 
+def test_swiglu_past_2_to_the_31_elements():
+    R, I = 70001, 16384
+    g = _gen(7)
+    gu = torch.empty((R, 2 * I), dtype=BF16, device="cuda")
+    gu.normal_(generator=g)
+    dh = torch.empty((R, I), dtype=BF16, device="cuda").normal_(generator=g)
+    w = torch.rand((R,), generator=g, device="cuda")
+    layer = moe.Moe(1, 64, I, 1)
+    h = layer.swiglu(gu, w)
+    dgu, dw = layer.swiglu_backward(dh, gu, w)
+    rows = [0, 65535, 65536, R - 1]
+    part = [t[rows].contiguous() for t in (gu, dh, w)]
+    small = layer.swiglu(part[0], part[2])
+    d_small, dw_small = layer.swiglu_backward(part[1], part[0], part[2])
+    assert torch.equal(h[rows], small) and torch.equal(dgu[rows], d_small) and torch.equal(dw[rows], dw_small)
+
+
 def test_swiglu_gradient_is_that_of_the_function():
     I = 128
     g = _gen(6)
@@ -310,6 +327,59 @@ def test_backward_is_the_gradient_of_the_forward():
         part = (grad.double() * v).flatten()
         # fp32 gradients: SUM of the terms; the difference: h^2 and 1e-16 / h of the loss
         assert (num - part.sum()).abs() <= 1e-5 * part.abs().sum() + 1e-6, name
+
+
+def test_norm_past_2_to_the_31_elements():
+    T, H = 140001, 16384
+    g = _gen(12)
+    resid = torch.empty((T, H), dtype=BF16, device="cuda").normal_(generator=g)
+    y = torch.empty((T, H), dtype=BF16, device="cuda").normal_(generator=g)
+    w = 1 + 0.1 * torch.randn((H,), generator=g, device="cuda")
+    layer = moe.Moe(1, H, 64, 1)
+    f = layer.block_norm(resid, y, w_post=w, gate=w, w_next=w)
+    rows = [0, 131071, 131072, T - 1]
+    s = layer.block_norm(resid[rows].contiguous(), y[rows].contiguous(), w_post=w, gate=w, w_next=w)
+    assert torch.equal(f["x"][rows], s["x"]) and torch.equal(f["resid"][rows], s["resid"])
+    kw = dict(w_post=w, gate=w, w_next=w)
+    b = layer.block_norm_backward(resid, f["x"], f["resid"], y, rstd_post=f["rstd_post"], rstd_next=f["rstd_next"], **kw)
+    c = layer.block_norm_backward(resid[rows].contiguous(), s["x"], s["resid"], y[rows].contiguous(),
+                                  rstd_post=s["rstd_post"], rstd_next=s["rstd_next"], **kw)
+    assert torch.equal(b["dresid"][rows], c["dresid"]) and torch.equal(b["dy"][rows], c["dy"])
+    assert layer.sync_status() == moe.MOE_OK
+
+
+def test_norm_captured_and_on_another_stream():
+    T, H = 700, 2880
+    a, g = _inputs(T, H, BF16, F32, True, True, True, 13)
+    dres, dx = _normal(g, (T, H)), _normal(g, (T, H))
+    layer = moe.Moe(1, H, 64, 1)
+
+    def step(stream=None):
+        f = layer.block_norm(**a, stream=stream)
+        b = layer.block_norm_backward(dres, dx, f["resid"], a["y"], rstd_post=f["rstd_post"], rstd_next=f["rstd_next"],
+                                      w_post=a["w_post"], gate=a["gate"], w_next=a["w_next"], stream=stream)
+        return list(f.values()) + list(b.values())
+
+    want = step()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = step(side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    # two captured graphs, replayed in turn and at once on two streams: workspaces of their own
+    graphs, outs = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step())
+    for _ in range(3):
+        side.wait_stream(torch.cuda.current_stream())
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(p, q) for p, q in zip(o, want))
 
 
 def test_no_rows():
