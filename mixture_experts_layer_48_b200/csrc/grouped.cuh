@@ -624,6 +624,16 @@ constexpr int kWgradThreads = kPairThreads + 64;   // + warps that mask ragged e
 static_assert(kPairSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
 static_assert(128 * 260 * 4 <= kPairStages * kPairStageBytes, "exchange of a split tile");
 
+// Arrives on the barrier at this offset in both CTAs of the pair (mask: their bits) when the
+// tcgen05 operations that this thread issued have completed.
+MOE_DEVINL void commit_pair(uint64_t* bar, uint16_t mask) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+      "%1;" ::"r"(smem_u32(bar)),
+      "h"(mask)
+      : "memory");
+}
+
 // One warp's 32 rows x 128 bytes (32 words w per lane, lane = row) to columns col0 .. of `out` (row
 // stride ld, first row row0), 16 rows at a time through shared memory so that eight lanes write
 // one whole 128-byte line (64 bytes a row ran at half HBM's write rate).  rows_ok: valid rows of
@@ -895,15 +905,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               tc_mma_bf16_2sm(d, adesc0 + soff + ((k16 * 32) >> 4),
                               bdesc0 + soff + ((k16 * kBStep) >> 4), idesc,
                               kst != p0 || k16 != 0);
-            const uint32_t e_local = smem_u32(&empty[slot]);
-            tc_commit_2sm(e_local);
-            tc_commit_2sm(mapa_shared(e_local, 1));
+            commit_pair(&empty[slot], 3);
             issued = true;
           }
           if (ok) {
-            const uint32_t f_local = smem_u32(&acc_full[buf]);
-            tc_commit_2sm(f_local);
-            tc_commit_2sm(mapa_shared(f_local, 1));
+            commit_pair(&acc_full[buf], 3);
           }
         }
       }
@@ -1136,15 +1142,11 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
             for (int k16 = 0; k16 < kGrBK / 16; ++k16)
               if (k16 < steps) tc_mma_bf16_2sm(d, adesc0 + soff + ((k16 * 2048) >> 4),
                               bdesc0 + soff + ((k16 * 2048) >> 4), idesc, r != p0 || k16 != 0);
-            const uint32_t e_local = smem_u32(&empty[slot]);
-            tc_commit_2sm(e_local);
-            tc_commit_2sm(mapa_shared(e_local, even + 1));
+            commit_pair(&empty[slot], (uint16_t)(3 << even));
             issued = true;
           }
           if (ok) {
-            const uint32_t f_local = smem_u32(&acc_full[buf]);
-            tc_commit_2sm(f_local);
-            tc_commit_2sm(mapa_shared(f_local, even + 1));
+            commit_pair(&acc_full[buf], (uint16_t)(3 << even));
           }
         }
       }
