@@ -879,9 +879,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const uint64_t bdesc0 = TRANS ? smem_desc_sw128(ring_s + kPairABytes, 16, 1024)
                                     : smem_desc_sw128(ring_s + kPairABytes, 64 * kGrBK * 2, 1024);
       constexpr int kBStep = TRANS ? 32 : 16 * 128;
-      uint32_t it = 0;
-      int unit = 0;
-      bool issued = false, ok = true;
+      // slot and phase are counted, not divided out: this lane's instructions bound the rate
+      int slot = 0, unit = 0;
+      uint32_t ph = 0, issued = 0;
+      bool ok = true;
       for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
         for (int p0 = 0; ok && p0 < nk; p0 += piece, ++unit) {
           const int p1 = min(nk, p0 + piece);
@@ -892,9 +893,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           }
           tc_fence_after();
           const uint32_t d = tmem_base + buf * 256;
-          for (int kst = p0; kst < p1; ++kst, ++it) {
-            const int slot = it % kPairStages;
-            if (!wait_or_abort(&full[slot], (it / kPairStages) & 1u, abort_flag, a.status)) {
+          uint32_t acc = 0;
+          for (int kst = p0; kst < p1; ++kst) {
+            if (!wait_or_abort(&full[slot], ph, abort_flag, a.status)) {
               ok = false;
               break;
             }
@@ -903,10 +904,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 #pragma unroll
             for (int k16 = 0; k16 < kGrBK / 16; ++k16)
               tc_mma_bf16_2sm(d, adesc0 + soff + ((k16 * 32) >> 4),
-                              bdesc0 + soff + ((k16 * kBStep) >> 4), idesc,
-                              kst != p0 || k16 != 0);
+                              bdesc0 + soff + ((k16 * kBStep) >> 4), idesc, acc | k16);
             commit_pair(&empty[slot], 3);
-            issued = true;
+            acc = issued = 1;
+            if (++slot == kPairStages) {
+              slot = 0;
+              ph ^= 1u;
+            }
           }
           if (ok) {
             commit_pair(&acc_full[buf], 3);
@@ -1105,9 +1109,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       const uint32_t ring_s = smem_u32(ring);
       const uint64_t adesc0 = smem_desc_sw128(ring_s, 64 * kGrBK * 2, 1024);
       const uint64_t bdesc0 = smem_desc_sw128(ring_s + kPairABytes, 64 * kGrBK * 2, 1024);
-      uint32_t it = 0, masked_ph = 0;   // bit s: parity of the next masked stage in slot s
-      int unit = 0;
-      bool issued = false, ok = true;
+      int slot = 0, unit = 0;
+      uint32_t ph = 0, issued = 0, masked_ph = 0;   // bit s: parity of the next masked stage in slot s
+      bool ok = true;
       for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
         const int cnt = seg.cnt[t / per];
         const Range rg = range_of(cnt);
@@ -1121,29 +1125,36 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
           }
           tc_fence_after();
           const uint32_t d = tmem_base + buf * 256;
-          for (int r = p0; r < p1; r += kGrBK, ++it) {
-            const int slot = it % kPairStages;
-            if (!wait_or_abort(&full[slot], (it / kPairStages) & 1u, abort_flag, a.status)) {
+          uint32_t acc = 0;
+          for (int r = p0; r < p1; r += kGrBK) {
+            if (!wait_or_abort(&full[slot], ph, abort_flag, a.status)) {
               ok = false;
               break;
             }
-            if (cnt - r < kGrBK) {
-              const uint32_t ph = (masked_ph >> slot) & 1u;
+            const uint64_t ak = adesc0 + ((slot * kPairStageBytes) >> 4);
+            const uint64_t bk = bdesc0 + ((slot * kPairStageBytes) >> 4);
+            if (cnt - r >= kGrBK) {
+              tc_fence_after();
+#pragma unroll
+              for (int k16 = 0; k16 < kGrBK / 16; ++k16)
+                tc_mma_bf16_2sm(d, ak + ((k16 * 2048) >> 4), bk + ((k16 * 2048) >> 4), idesc, acc | k16);
+            } else {
+              const uint32_t mph = (masked_ph >> slot) & 1u;
               masked_ph ^= 1u << slot;
-              if (!wait_or_abort_cluster(&peer_masked[slot], ph, abort_flag, a.status)) {
+              if (!wait_or_abort_cluster(&peer_masked[slot], mph, abort_flag, a.status)) {
                 ok = false;
                 break;
               }
+              tc_fence_after();
+              for (int k16 = 0; k16 < (cnt - r + 15) / 16; ++k16)
+                tc_mma_bf16_2sm(d, ak + ((k16 * 2048) >> 4), bk + ((k16 * 2048) >> 4), idesc, acc | k16);
             }
-            tc_fence_after();
-            const uint64_t soff = (uint64_t)((slot * kPairStageBytes) >> 4);
-            const int steps = min(kGrBK / 16, (cnt - r + 15) / 16);
-#pragma unroll
-            for (int k16 = 0; k16 < kGrBK / 16; ++k16)
-              if (k16 < steps) tc_mma_bf16_2sm(d, adesc0 + soff + ((k16 * 2048) >> 4),
-                              bdesc0 + soff + ((k16 * 2048) >> 4), idesc, r != p0 || k16 != 0);
             commit_pair(&empty[slot], (uint16_t)(3 << even));
-            issued = true;
+            acc = issued = 1;
+            if (++slot == kPairStages) {
+              slot = 0;
+              ph ^= 1u;
+            }
           }
           if (ok) {
             commit_pair(&acc_full[buf], (uint16_t)(3 << even));
