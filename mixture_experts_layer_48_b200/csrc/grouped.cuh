@@ -833,25 +833,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 0) {
     // ------------------------------ TMA producer (both CTAs) ------------------------------
     if (lane == 0) {
-      uint32_t it = 0;
-      int last_it[kPairStages];
-#pragma unroll
-      for (int s = 0; s < kPairStages; ++s) last_it[s] = -1;
-      for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+      const uint32_t full0 = mapa_shared(smem_u32(full), 0);   // the even CTA's full[0]
+      uint32_t issued = 0, ph = 0;
+      int slot = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
         const Tile w = tile_at(t);
         const int row0 = w.row0 + rank * kPairHalf, col0 = w.n0 + rank * kPairHalf;
-        bool ok = true;
-        for (int kst = 0; kst < nk; ++kst, ++it) {
-          const int slot = it % kPairStages;
-          const uint32_t ph = (it / kPairStages) & 1u;
+        for (int k = 0; k < a.Kred; k += kGrBK) {
           if (!wait_or_abort(&empty[slot], ph ^ 1u, abort_flag, a.status)) {
             ok = false;
             break;
           }
-          const uint32_t bar = mapa_shared(smem_u32(&full[slot]), 0);
+          const uint32_t bar = full0 + 8 * slot;
           if (leader) mbar_arrive_expect_tx(&full[slot], 2 * kPairStageBytes);
           uint8_t* st = ring + slot * kPairStageBytes;
-          const int k = kst * kGrBK;
           tma_load_2d_pair(st, &xmap, k, row0, bar);
           if (TRANS) {
             tma_load_3d_pair(st + kPairABytes, &wmap, k, col0, w.e, bar);
@@ -859,15 +855,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
             tma_load_3d_pair(st + kPairABytes, &wmap, col0, k, w.e, bar);
             tma_load_3d_pair(st + kPairABytes + 64 * kGrBK * 2, &wmap, col0 + 64, k, w.e, bar);
           }
-          last_it[slot] = it;
+          ++issued;
+          if (++slot == kPairStages) {
+            slot = 0;
+            ph ^= 1u;
+          }
         }
-        if (!ok) break;
       }
       // the even CTA's full barriers count both CTAs' copies: drain them before the pair exits
       if (leader)
-        for (int s = 0; s < kPairStages; ++s)
-          if (last_it[s] >= 0 &&
-              !mbar_wait_bounded(&full[s], (last_it[s] / kPairStages) & 1u, kWaitLimitNs))
+        for (uint32_t j = issued - min(issued, (uint32_t)kPairStages); j < issued; ++j)
+          if (!mbar_wait_bounded(&full[j % kPairStages], (j / kPairStages) & 1u, kWaitLimitNs))
             atomicOr(a.status, kStatusTimeout);
     }
   } else if (warp == 1) {
@@ -1050,27 +1048,26 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
   if (warp == 0) {
     // ------------------------------ TMA producer (both CTAs) ------------------------------
     if (lane == 0) {
-      uint32_t it = 0, ragged_ph = 0;   // bit s: parity of the next masked stage in slot s
-      uint32_t last_ragged = 0;         // bit s: slot s's last stage was a masked one
-      int last_it[kPairStages];
-#pragma unroll
-      for (int s = 0; s < kPairStages; ++s) last_it[s] = -1;
-      for (int t = pair; t < tiles && !*abort_flag; t += npairs) {
+      const uint32_t full0 = mapa_shared(smem_u32(full), even);   // the even CTA's full[0]
+      uint32_t issued = 0, ph = 0;
+      uint32_t ragged_ph = 0;     // bit s: parity of the next masked stage in slot s
+      uint32_t last_ragged = 0;   // bit s: slot s's last stage was a masked one
+      int slot = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
         const int e = t / per, l = t - e * per;
         const int m0 = l / NT * 256 + rank * kPairHalf, n0 = l % NT * 256 + rank * kPairHalf;
         const int beg = seg.beg[e], cnt = seg.cnt[e];
         const Range rg = range_of(cnt);
-        bool ok = true;
-        for (int r = rg.r0; r < rg.r1; r += kGrBK, ++it) {
-          const int slot = it % kPairStages;
-          if (!wait_or_abort(&empty[slot], ((it / kPairStages) & 1u) ^ 1u, abort_flag, a.status)) {
+        for (int r = rg.r0; r < rg.r1; r += kGrBK) {
+          if (!wait_or_abort(&empty[slot], ph ^ 1u, abort_flag, a.status)) {
             ok = false;
             break;
           }
           uint8_t* st = ring + slot * kPairStageBytes;
           constexpr int kBox = 64 * kGrBK * 2;
           if (cnt - r >= kGrBK) {
-            const uint32_t bar = mapa_shared(smem_u32(&full[slot]), even);
+            const uint32_t bar = full0 + 8 * slot;
             if (leader) mbar_arrive_expect_tx(&full[slot], 2 * kPairStageBytes);
             tma_load_2d_pair(st, &xmap, m0, beg + r, bar);
             tma_load_2d_pair(st + kBox, &xmap, m0 + 64, beg + r, bar);
@@ -1086,19 +1083,21 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
             last_ragged |= 1u << slot;
             ragged_ph ^= 1u << slot;
           }
-          last_it[slot] = it;
+          ++issued;
+          if (++slot == kPairStages) {
+            slot = 0;
+            ph ^= 1u;
+          }
         }
-        if (!ok) break;
       }
       // drain: a masked stage's copies are this CTA's own, the others are counted on the even
       // CTA's full barriers
-      for (int s = 0; s < kPairStages; ++s) {
-        if (last_it[s] < 0) continue;
+      for (uint32_t j = issued - min(issued, (uint32_t)kPairStages); j < issued; ++j) {
+        const int s = j % kPairStages;
         bool done = true;
         if ((last_ragged >> s) & 1u)
           done = mbar_wait_bounded(&ragged[s], ((ragged_ph >> s) & 1u) ^ 1u, kWaitLimitNs);
-        if (leader)
-          done = mbar_wait_bounded(&full[s], (last_it[s] / kPairStages) & 1u, kWaitLimitNs) && done;
+        if (leader) done = mbar_wait_bounded(&full[s], (j / kPairStages) & 1u, kWaitLimitNs) && done;
         if (!done) atomicOr(a.status, kStatusTimeout);
       }
     }
