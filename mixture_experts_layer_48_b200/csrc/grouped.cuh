@@ -624,6 +624,11 @@ constexpr int kWgradThreads = kPairThreads + 64;   // + warps that mask ragged e
 static_assert(kPairSmem + (int)sizeof(Segments) + 64 <= 227 * 1024, "shared memory");
 static_assert(128 * 260 * 4 <= kPairStages * kPairStageBytes, "exchange of a split tile");
 
+// Half of the columns of a matrix's last 256-column block, rounded up to 16: what each CTA stages of
+// it, so that the block's MMAs cover no more columns than it holds (2880 columns end in a block of
+// 64).  The block of tile t is t % NT in both kernels.
+MOE_DEVINL int last_half(int ncols, int NT) { return (ncols - 256 * (NT - 1) + 31) / 32 * 16; }
+
 // Arrives on the barrier at this offset in both CTAs of the pair (mask: their bits) when the
 // tcgen05 operations that this thread issued have completed.
 MOE_DEVINL void commit_pair(uint64_t* bar, uint16_t mask) {
@@ -839,21 +844,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       bool ok = true;
       for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
         const Tile w = tile_at(t);
-        const int row0 = w.row0 + rank * kPairHalf, col0 = w.n0 + rank * kPairHalf;
+        const int half = t % NT == NT - 1 ? last_half(a.Ncols, NT) : kPairHalf;
+        const int row0 = w.row0 + rank * kPairHalf, col0 = w.n0 + rank * half;
+        const bool two = !TRANS && half > 64;   // 64-column boxes
+        const uint32_t bytes = kPairABytes + (TRANS || two ? kPairABytes : kPairABytes / 2);
         for (int k = 0; k < a.Kred; k += kGrBK) {
           if (!wait_or_abort(&empty[slot], ph ^ 1u, abort_flag, a.status)) {
             ok = false;
             break;
           }
           const uint32_t bar = full0 + 8 * slot;
-          if (leader) mbar_arrive_expect_tx(&full[slot], 2 * kPairStageBytes);
+          if (leader) mbar_arrive_expect_tx(&full[slot], 2 * bytes);
           uint8_t* st = ring + slot * kPairStageBytes;
           tma_load_2d_pair(st, &xmap, k, row0, bar);
           if (TRANS) {
             tma_load_3d_pair(st + kPairABytes, &wmap, k, col0, w.e, bar);
           } else {
             tma_load_3d_pair(st + kPairABytes, &wmap, col0, k, w.e, bar);
-            tma_load_3d_pair(st + kPairABytes + 64 * kGrBK * 2, &wmap, col0 + 64, k, w.e, bar);
+            if (two)
+              tma_load_3d_pair(st + kPairABytes + 64 * kGrBK * 2, &wmap, col0 + 64, k, w.e, bar);
           }
           ++issued;
           if (++slot == kPairStages) {
@@ -871,7 +880,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     // ------------------------------ MMA issuer (even CTA) ------------------------------
     if (leader && lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, false, !TRANS);
+      constexpr uint32_t idesc_all = idesc_bf16_f32(256, 256, false, !TRANS);
+      const uint32_t idesc_last = idesc_bf16_f32(256, 2 * last_half(a.Ncols, NT), false, !TRANS);
       const uint32_t ring_s = smem_u32(ring);
       const uint64_t adesc0 = smem_desc_sw128(ring_s, 16, 1024);
       const uint64_t bdesc0 = TRANS ? smem_desc_sw128(ring_s + kPairABytes, 16, 1024)
@@ -882,6 +892,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       uint32_t ph = 0, issued = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
+        const uint32_t idesc = t % NT == NT - 1 ? idesc_last : idesc_all;
         for (int p0 = 0; ok && p0 < nk; p0 += piece, ++unit) {
           const int p1 = min(nk, p0 + piece);
           const int buf = unit & 1;
@@ -1056,7 +1067,10 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       bool ok = true;
       for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
         const int e = t / per, l = t - e * per;
-        const int m0 = l / NT * 256 + rank * kPairHalf, n0 = l % NT * 256 + rank * kPairHalf;
+        const int half = t % NT == NT - 1 ? last_half(a.Ncols, NT) : kPairHalf;
+        const int m0 = l / NT * 256 + rank * kPairHalf, n0 = l % NT * 256 + rank * half;
+        const bool two = half > 64;   // 64-column boxes
+        const uint32_t bytes = kPairABytes + (two ? kPairABytes : kPairABytes / 2);
         const int beg = seg.beg[e], cnt = seg.cnt[e];
         const Range rg = range_of(cnt);
         for (int r = rg.r0; r < rg.r1; r += kGrBK) {
@@ -1068,18 +1082,18 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
           constexpr int kBox = 64 * kGrBK * 2;
           if (cnt - r >= kGrBK) {
             const uint32_t bar = full0 + 8 * slot;
-            if (leader) mbar_arrive_expect_tx(&full[slot], 2 * kPairStageBytes);
+            if (leader) mbar_arrive_expect_tx(&full[slot], 2 * bytes);
             tma_load_2d_pair(st, &xmap, m0, beg + r, bar);
             tma_load_2d_pair(st + kBox, &xmap, m0 + 64, beg + r, bar);
             tma_load_2d_pair(st + 2 * kBox, &dymap, n0, beg + r, bar);
-            tma_load_2d_pair(st + 3 * kBox, &dymap, n0 + 64, beg + r, bar);
+            if (two) tma_load_2d_pair(st + 3 * kBox, &dymap, n0 + 64, beg + r, bar);
             last_ragged &= ~(1u << slot);
           } else {
-            mbar_arrive_expect_tx(&ragged[slot], kPairStageBytes);
+            mbar_arrive_expect_tx(&ragged[slot], bytes);
             tma_load_2d(st, &xmap, m0, beg + r, &ragged[slot]);
             tma_load_2d(st + kBox, &xmap, m0 + 64, beg + r, &ragged[slot]);
             tma_load_2d(st + 2 * kBox, &dymap, n0, beg + r, &ragged[slot]);
-            tma_load_2d(st + 3 * kBox, &dymap, n0 + 64, beg + r, &ragged[slot]);
+            if (two) tma_load_2d(st + 3 * kBox, &dymap, n0 + 64, beg + r, &ragged[slot]);
             last_ragged |= 1u << slot;
             ragged_ph ^= 1u << slot;
           }
@@ -1104,7 +1118,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
   } else if (warp == 1) {
     // ------------------------------ MMA issuer (even CTA) ------------------------------
     if (leader && lane == 0) {
-      constexpr uint32_t idesc = idesc_bf16_f32(256, 256, true, true);
+      constexpr uint32_t idesc_all = idesc_bf16_f32(256, 256, true, true);
+      const uint32_t idesc_last = idesc_bf16_f32(256, 2 * last_half(a.Ncols, NT), true, true);
       const uint32_t ring_s = smem_u32(ring);
       const uint64_t adesc0 = smem_desc_sw128(ring_s, 64 * kGrBK * 2, 1024);
       const uint64_t bdesc0 = smem_desc_sw128(ring_s + kPairABytes, 64 * kGrBK * 2, 1024);
@@ -1113,6 +1128,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       bool ok = true;
       for (int t = pair; ok && t < tiles && !*abort_flag; t += npairs) {
         const int cnt = seg.cnt[t / per];
+        const uint32_t idesc = t % NT == NT - 1 ? idesc_last : idesc_all;
         const Range rg = range_of(cnt);
         const int piece = F32 ? kGrPieceStages * kGrBK : max(cnt, 1);
         for (int p0 = rg.r0; ok && p0 < rg.r1; p0 += piece, ++unit) {
