@@ -21,6 +21,16 @@
 //   grouped_wgrad_kernel  256 x 256 tiles of dW[e] per CTA pair, the expert's rows are the
 //                         reduction; both operands are MN-major
 //
+// Measured (graph replay, one B200; copy bandwidth 6.46 TB/s, bf16 1.63 PFLOP/s in a burst and
+// 1.38 sustained):
+//   grouped_cols_kernel   64 rows over 32 experts, 2880 x 5760: 144 us, 6.5 TB/s; one token on 128
+//                         experts, 2880 x 2880, fp32: 20.1 us, 3.3 TB/s (about 5 us of it start-up)
+//   grouped_rows_kernel   131,072 skewed rows, 2880 x 5760: 3.4 ms, 1.27 PFLOP/s; tensor pipe 85 %
+//                         busy, the rest is hand-over and the experts' padded last chunks
+//   grouped_wgrad_kernel  32,768 rows, 2880 x 5760: 1.0 ms, 1.06 PFLOP/s; tensor pipe 62 % busy
+//                         (16 stages a tile, each with a ragged end); 512 rows over 128 experts,
+//                         2880 x 2880: 462 us, 4.6 TB/s of writes
+//
 // The segments are read on the device: every CTA checks the E + 1 offsets and scans them in
 // shared memory, so there is no work-list kernel, no workspace and no host sync.  Offsets that
 // are negative, decrease or pass R give empty segments and set the status word.  Rows outside
