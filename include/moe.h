@@ -341,6 +341,10 @@ MOE_API moe_status moe_route_static(moe_t ctx, int T, const void* x_bf16,
  *              dW_gate_up = x_perm^T dgu;  dx = combine(dx_perm)
  * All of them run on the current device, which must be the handle's (MOE_ERR_ARG otherwise), and
  * only enqueue work on `stream`; none allocates, synchronises or keeps anything between calls.
+ * Tensors are row-major without gaps and, as everywhere, 16-byte aligned; offsets, the per-row
+ * arrays (row_w, drow_w, rstd_*) and the vectors' gradients (dw_*, dgate) only need 4 bytes, so
+ * they may be parts of larger arrays.  Buffers that a call writes overlap none of its others unless
+ * it says so.
  * Every sum is fp32; results of one build on one device do not change from call to call. */
 typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
 
@@ -387,8 +391,8 @@ MOE_API moe_status moe_swiglu_backward(moe_t ctx, int R, const void* dh_bf16, co
  * y NULL: the norm before a first block alone, x = resid / rms(resid) * w_next (then w_post, gate,
  * resid_out and rstd_post are NULL).  resid and resid_out [T, H] are of resid_type, y [T, H] of
  * y_type, x [T, H] bf16; w_post, gate, w_next [H] fp32; rstd_post (with w_post) and rstd_next (with
- * w_next) [T] fp32 receive 1 / rms for the backward pass.  resid_out may be resid itself; no other
- * buffers may overlap.  0 <= T <= 2^20.
+ * w_next) [T] fp32 receive 1 / rms for the backward pass.  resid_out may be resid itself.
+ * 0 <= T <= 2^20.
  *
  * Backward: dresid [T, H] is the gradient that reaches resid_out from elsewhere (NULL: none; it
  * may only be NULL with w_next), dx that of x; resid is the forward call's resid_out (its resid

@@ -4,13 +4,15 @@
 //
 // One row is spread over TPR threads, VPT vectors of 4 (or 8) consecutive elements each, and
 // stays in registers between the passes over it, so every input is read once and every output
-// written once.  Measured (graph replay, one B200, copy bandwidth 6.46 TB/s; rows of 2880):
-// SwiGLU 32,768 rows 86 us forward, 138 us backward (6.6 and 6.8 TB/s); norms of 8189 rows, bf16
-// residual and fp32 block output, 42 us forward (5.6 TB/s: issue slots and row sums), 32,768 fp32
-// rows backward 279 us (6.75 TB/s).  All arithmetic and every sum is fp32.  Sums over rows (the gradients of the
-// norm weights and the gate) are kept in registers per thread over all rows of a persistent
-// block, written as one partial row per row group and added in a fixed order by a second kernel:
-// results do not depend on timing.
+// written once.  All arithmetic and every sum is fp32.  Sums over rows (the gradients of the norm
+// weights and the gate) are kept in registers per thread over all rows of a persistent block,
+// written as one partial row per row group and added in a fixed order by a second kernel: results
+// do not depend on timing.
+//
+// Measured (graph replay, one B200, copy bandwidth 6.46 TB/s; rows of 2880): SwiGLU of 32,768 rows
+// 86 us forward, 138 us backward (6.6 and 6.8 TB/s); norms of 8189 rows, bf16 residual and fp32
+// block output, 42 us forward (5.6 TB/s: issue slots and row sums), of 32,768 fp32 rows 279 us
+// backward (6.75 TB/s).
 #pragma once
 
 #include "common.cuh"

@@ -19,6 +19,12 @@ bool on_device(const moe_ctx* c) {
   return dev == c->device;
 }
 
+// Arrays that kernels read one element at a time: offsets, per-row weights and norms.
+bool all_aligned4(std::initializer_list<const void*> ps) {  // null passes
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return false;
+  return true;
+}
 bool all_aligned16(std::initializer_list<const void*> ps) {  // null passes
   for (const void* p : ps)
     if (!aligned16(p)) return false;
@@ -313,7 +319,8 @@ moe_status moe_grouped_matmul(moe_t c, int R, int K, int N, int transpose, const
   if (!c || !grouped_shape_ok(c, R, K, N, out_type)) return MOE_ERR_ARG;
   if (R == 0) return MOE_OK;
   if (!offsets || !x_rows_bf16 || !W_bf16 || !out) return MOE_ERR_ARG;
-  if (!all_aligned16({offsets, x_rows_bf16, W_bf16, out}) || !on_device(c)) return MOE_ERR_ARG;
+  if (!all_aligned4({offsets}) || !all_aligned16({x_rows_bf16, W_bf16, out}) || !on_device(c))
+    return MOE_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   GroupedArgs a{};
   a.offsets = offsets;
@@ -341,7 +348,7 @@ moe_status moe_grouped_wgrad(moe_t c, int R, int K, int N, const int32_t* offset
     return cudaMemsetAsync(dW, 0, bytes, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   }
   if (!offsets || !x_rows_bf16 || !dy_rows_bf16 ||
-      !all_aligned16({offsets, x_rows_bf16, dy_rows_bf16}))
+      !all_aligned4({offsets}) || !all_aligned16({x_rows_bf16, dy_rows_bf16}))
     return MOE_ERR_ARG;
   GroupedArgs a{};
   a.offsets = offsets;
@@ -375,7 +382,8 @@ moe_status moe_swiglu(moe_t c, int R, const void* gu_bf16, const float* row_w, v
                       moe_stream_t stream) {
   if (!c || R < 0 || R > kMaxRows) return MOE_ERR_ARG;
   if (R == 0) return MOE_OK;
-  if (!gu_bf16 || !h_bf16 || !all_aligned16({gu_bf16, row_w, h_bf16}) || !on_device(c))
+  if (!gu_bf16 || !h_bf16 || !all_aligned4({row_w}) || !all_aligned16({gu_bf16, h_bf16}) ||
+      !on_device(c))
     return MOE_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const long long blocks = ((long long)R * (c->I / 8) + 255) / 256;
@@ -392,7 +400,8 @@ moe_status moe_swiglu_backward(moe_t c, int R, const void* dh_bf16, const void* 
   if (!c || R < 0 || R > kMaxRows) return MOE_ERR_ARG;
   if (R == 0) return MOE_OK;
   if (!dh_bf16 || !gu_bf16 || !dgu_bf16 || (drow_w && !row_w) ||
-      !all_aligned16({dh_bf16, gu_bf16, row_w, dgu_bf16, drow_w}) || !on_device(c))
+      !all_aligned4({row_w, drow_w}) || !all_aligned16({dh_bf16, gu_bf16, dgu_bf16}) ||
+      !on_device(c))
     return MOE_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   return by_row_length(c->I / 8, [&](auto tpr, auto vpt) {   // vectors of 8
@@ -420,8 +429,8 @@ moe_status moe_block_norm(moe_t c, int T, moe_dtype resid_type, moe_dtype y_type
   if ((w_post != nullptr) != (rstd_post != nullptr)) return MOE_ERR_ARG;
   if ((w_next != nullptr) != (x_bf16 != nullptr) || (w_next != nullptr) != (rstd_next != nullptr))
     return MOE_ERR_ARG;
-  if (!all_aligned16({resid, y, w_post, gate, w_next, resid_out, x_bf16, rstd_post, rstd_next}) ||
-      !on_device(c))
+  if (!all_aligned4({rstd_post, rstd_next}) ||
+      !all_aligned16({resid, y, w_post, gate, w_next, resid_out, x_bf16}) || !on_device(c))
     return MOE_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   NormArgs a{};
@@ -489,8 +498,8 @@ moe_status moe_block_norm_backward(moe_t c, int T, moe_dtype resid_type, moe_dty
     if (post != (rstd_post != nullptr) || ((post || gated) && (!y || !dy))) return MOE_ERR_ARG;
     if (!dresid_out || (!next && !dy) || (!next && !dresid)) return MOE_ERR_ARG;
   }
-  if (!all_aligned16({dresid, dx_bf16, resid, y, rstd_post, rstd_next, w_post, gate, w_next,
-                      dresid_out, dy, dw_post, dgate, dw_next}) ||
+  if (!all_aligned4({rstd_post, rstd_next, dw_post, dgate, dw_next}) ||
+      !all_aligned16({dresid, dx_bf16, resid, y, w_post, gate, w_next, dresid_out, dy}) ||
       !on_device(c))
     return MOE_ERR_ARG;
   const bool sums = next || post || gated;

@@ -346,6 +346,10 @@ def test_refusals():
         layer.grouped_matmul(x, torch.zeros((4, 64, 12), dtype=BF16, device="cuda"), o)
     with pytest.raises(moe.MoeError):   # a row length of 2 bytes' alignment
         layer.grouped_matmul(torch.zeros((6 * 64 + 1,), dtype=BF16, device="cuda")[1:].view(6, 64), W, o)
+    # offsets and per-row arrays may be parts of larger ones
+    many = torch.zeros((3, 5), dtype=torch.int32, device="cuda")
+    layer.grouped_matmul(x, W, many[1])
+    layer.grouped_wgrad(x, x, many[1])
     p = lambda t: t.data_ptr()  # noqa: E731
     out = torch.zeros((6, 72), dtype=BF16, device="cuda")
     call = lambda *a: moe.moe_grouped_matmul(layer.handle, *a, None)  # noqa: E731

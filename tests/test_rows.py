@@ -125,6 +125,7 @@ def test_swiglu_out_argument_and_refusals():
             layer.swiglu(**bad)
     with pytest.raises(ValueError):
         layer.swiglu_backward(out[:3], gu)
+    assert torch.equal(layer.swiglu(gu, torch.ones((5,), device="cuda")[1:]), layer.swiglu(gu, w))
     assert layer.swiglu(gu[:0]).shape == (0, 128)
     d, dw = layer.swiglu_backward(out[:0], gu[:0], w[:0])
     assert d.shape == (0, 256) and dw.shape == (0,)
