@@ -349,27 +349,22 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
   if (warp == 0) {
     // ------------------------------ TMA producer ------------------------------
     if (lane == 0) {
-      uint32_t it = 0;
-      int last_it[kStages];
-#pragma unroll
-      for (int s = 0; s < kStages; ++s) last_it[s] = -1;
-      for (int t = group; t < tiles && !*abort_flag; t += groups) {
+      uint32_t issued = 0, ph = 0;
+      int slot = 0;
+      bool ok = true;
+      for (int t = group; ok && t < tiles && !*abort_flag; t += groups) {
         const Tile w = tile_at(t);
         int k0, k1;
         k_range(t, k0, k1);
         const int nrb = (w.rows + C::kRowBox - 1) / C::kRowBox;
         const uint32_t bytes = C::kABytes + (uint32_t)nrb * C::kRowBox * kGrBK * 2;
-        bool ok = true;
-        for (int kst = k0; kst < k1; ++kst, ++it) {
-          const int slot = it % kStages;
-          const uint32_t ph = (it / kStages) & 1u;
+        for (int k = k0 * kGrBK; k < k1 * kGrBK; k += kGrBK) {
           if (!wait_or_abort(&empty[slot], ph ^ 1u, abort_flag, a.status)) {
             ok = false;
             break;
           }
           mbar_arrive_expect_tx(&full[slot], bytes);
           uint8_t* st = ring + slot * C::kStageBytes;
-          const int k = kst * kGrBK;
           // weight boxes past the matrix's edges are zero-filled (each expert is a plane of the
           // map, so an edge never reads the next expert)
           if (TRANS) {  // [columns of y, reduction]: 128 x 64 boxes, K-major
@@ -384,14 +379,16 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
           for (int r = 0; r < nrb; ++r)
             tma_load_2d(st + C::kABytes + r * (C::kRowBox * kGrBK * 2), &xmap, k,
                         w.row0 + r * C::kRowBox, &full[slot]);
-          last_it[slot] = it;
+          ++issued;
+          if (++slot == kStages) {
+            slot = 0;
+            ph ^= 1u;
+          }
         }
-        if (!ok) break;
       }
       // never leave the CTA with copies in flight
-      for (int s = 0; s < kStages; ++s)
-        if (last_it[s] >= 0 &&
-            !mbar_wait_bounded(&full[s], (last_it[s] / kStages) & 1u, kWaitLimitNs))
+      for (uint32_t j = issued - min(issued, (uint32_t)kStages); j < issued; ++j)
+        if (!mbar_wait_bounded(&full[j % kStages], (j / kStages) & 1u, kWaitLimitNs))
           atomicOr(a.status, kStatusTimeout);
     }
   } else if (warp == 1) {
@@ -403,9 +400,9 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
                                     : smem_desc_sw128(ring_s, 64 * kGrBK * 2, 1024);
       const uint64_t bdesc0 = smem_desc_sw128(ring_s + C::kABytes, 16, 1024);
       constexpr int kAStep = TRANS ? 32 : 16 * 128;    // bytes per 16 reduction elements
-      uint32_t it = 0;
-      int unit = 0;
-      bool issued = false, ok = true;
+      int slot = 0, unit = 0;
+      uint32_t ph = 0, issued = 0;
+      bool ok = true;
       for (int t = group; ok && t < tiles && !*abort_flag; t += groups) {
         const Tile w = tile_at(t);
         int k0, k1;
@@ -422,9 +419,8 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
           }
           tc_fence_after();
           const uint32_t d = tmem_base + buf * NM * ROWS;
-          for (int kst = p0; kst < p1; ++kst, ++it) {
-            const int slot = it % kStages;
-            const uint32_t ph = (it / kStages) & 1u;
+          uint32_t acc = 0;
+          for (int kst = p0; kst < p1; ++kst) {
             if (!wait_or_abort(&full[slot], ph, abort_flag, a.status)) {
               ok = false;
               break;
@@ -435,13 +431,16 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
             for (int k16 = 0; k16 < kGrBK / 16; ++k16) {
               const uint64_t ak = adesc0 + soff + ((k16 * kAStep) >> 4);
               const uint64_t bk = bdesc0 + soff + ((k16 * 32) >> 4);
-              const uint32_t acc = kst != p0 || k16 != 0;
 #pragma unroll
               for (int m = 0; m < NM; ++m)
-                tc_mma_bf16(d + m * ROWS, ak + ((m * 128 * kGrBK * 2) >> 4), bk, idesc, acc);
+                tc_mma_bf16(d + m * ROWS, ak + ((m * 128 * kGrBK * 2) >> 4), bk, idesc, acc | k16);
             }
             tc_commit(&empty[slot]);
-            issued = true;
+            acc = issued = 1;
+            if (++slot == kStages) {
+              slot = 0;
+              ph ^= 1u;
+            }
           }
           if (ok) tc_commit(&acc_full[buf]);
         }
