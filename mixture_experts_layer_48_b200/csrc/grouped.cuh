@@ -555,8 +555,9 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
             ++unit;
           }
         }
-        // a tile is added up after the next one's sums have left
-        if (ti > 0) ok = add_parts(prev, ti - 1, ok);
+        // a tile is added up after the next one's sums have left; either way the four warps agree
+        // on going on (they meet at the same barriers)
+        ok = ti > 0 ? add_parts(prev, ti - 1, ok) : named_bar_and(1, 128, ok);
         prev = w;
         if (!ok) break;
       } else if (ok) {
