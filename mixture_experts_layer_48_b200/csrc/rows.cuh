@@ -108,15 +108,16 @@ MOE_DEVINL float4 post_factor(const NormArgs& a, int v) {
   return p;
 }
 
-// Blocks per SM of the staged kernels: 1024 threads forward (64 registers each) and 512 backward
-// (128) with up to three vectors a thread, else one block.
+// Blocks per SM of the staged kernels, by the registers that a thread's vectors take: forward 1024
+// threads (64 registers) with three vectors a thread, 1280 (51) with fewer; backward 512 (128), 640
+// (102) and 1024 (64).  More vectors: one block.
 template <int TPR, int VPT>
 constexpr int norm_forward_blocks() {
-  return VPT > 3 ? 1 : 1024 / RowCfg<TPR, VPT>::kThreads;
+  return VPT > 3 ? 1 : (VPT == 3 ? 1024 : 1280) / RowCfg<TPR, VPT>::kThreads;
 }
 template <int TPR, int VPT>
 constexpr int norm_backward_blocks() {
-  return VPT > 3 ? 1 : 512 / RowCfg<TPR, VPT>::kThreads;
+  return VPT > 3 ? 1 : (VPT == 3 ? 512 : VPT == 2 ? 640 : 1024) / RowCfg<TPR, VPT>::kThreads;
 }
 constexpr int kRowRingMax = 4;
 
