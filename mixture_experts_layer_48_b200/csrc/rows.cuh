@@ -117,7 +117,7 @@ constexpr int norm_forward_blocks() {
 }
 template <int TPR, int VPT>
 constexpr int norm_backward_blocks() {
-  return VPT > 3 ? 1 : (VPT == 3 ? 512 : VPT == 2 ? 640 : 1024) / RowCfg<TPR, VPT>::kThreads;
+  return VPT > 3 ? 1 : (VPT == 3 ? 512 : VPT == 2 ? 768 : 1024) / RowCfg<TPR, VPT>::kThreads;
 }
 constexpr int kRowRingMax = 4;
 
