@@ -109,15 +109,17 @@ MOE_DEVINL float4 post_factor(const NormArgs& a, int v) {
 }
 
 // Blocks per SM of the staged kernels, by the registers that a thread's vectors take: forward 1024
-// threads (64 registers) with three vectors a thread, 1280 (51) with fewer; backward 512 (128), 640
-// (102) and 1024 (64).  More vectors: one block.
+// threads (64 registers) with three vectors a thread, 1280 (51) with fewer; backward 512 (128), 768
+// (85) and 1024 (64).  A backward row on 512 threads with two vectors takes two blocks of 64
+// registers, some of them spilled (16,000 rows of 4096: 199 us, 217 with one block).  More vectors:
+// one block.
 template <int TPR, int VPT>
 constexpr int norm_forward_blocks() {
   return VPT > 3 ? 1 : (VPT == 3 ? 1024 : 1280) / RowCfg<TPR, VPT>::kThreads;
 }
 template <int TPR, int VPT>
 constexpr int norm_backward_blocks() {
-  return VPT > 3 ? 1 : (VPT == 3 ? 512 : VPT == 2 ? 768 : 1024) / RowCfg<TPR, VPT>::kThreads;
+  return VPT > 3 ? 1 : (VPT == 3 ? 512 : VPT == 2 && TPR < 512 ? 768 : 1024) / RowCfg<TPR, VPT>::kThreads;
 }
 constexpr int kRowRingMax = 4;
 
