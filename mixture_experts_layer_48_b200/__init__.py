@@ -291,8 +291,9 @@ class Moe:
 
     # -- training and the block around the layer (include/moe.h) ------------------------
     # A call with stream= runs as one inside torch.cuda.stream(stream): what it allocates (results,
-    # workspaces) belongs to the stream it enqueues on.  Tensors must be on the handle's device,
-    # which must be the current one.
+    # workspaces) belongs to the stream it enqueues on.  Its arguments are the caller's to order
+    # and to keep for that stream, as for any torch operation.  Tensors must be on the handle's
+    # device, which must be the current one.
     def _arg(self, t, dtype, name: str, shape) -> int:
         """Address of an argument after its checks; 0 for None."""
         if t is None:
