@@ -233,10 +233,12 @@ MOE_DEVINL void store4(void* out, size_t idx, float4 v) {
 template <int ROWS, int NM>
 struct ColsCfg {
   static constexpr bool kSplit = NM == 1;
-  static constexpr int kABytes = NM * 128 * kGrBK * 2;
-  static constexpr int kBBytes = ROWS * kGrBK * 2;
+  static constexpr int kK = kSplit ? 2 * kGrBK : kGrBK;     // reduction elements per stage
+  static constexpr int kABytes = NM * 128 * kK * 2;
+  static constexpr int kBHalf = ROWS * kGrBK * 2;           // 64 elements of every row
+  static constexpr int kBBytes = ROWS * kK * 2;
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = kSplit ? 9 : 4;
+  static constexpr int kStages = 4;
   // Rows per TMA box: the MMAs take the rows rounded up to 16; a 128-row tile copies 64 at a time
   // (8 experts of 128 rows, 2880 x 2880: 30.1 us against 37.1 with boxes of 16).
   static constexpr int kRowBox = kSplit ? 16 : 64;
@@ -312,8 +314,8 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
 
   const int NT = (a.Ncols + TW - 1) / TW;
   const int tiles = seg.base[a.E] * NT;
-  const int nk_all = (a.Kred + kGrBK - 1) / kGrBK;
-  const int piece = F32 ? kGrPieceStages : nk_all;
+  const int nk_all = (a.Kred + C::kK - 1) / C::kK;
+  const int piece = F32 ? kGrPieceStages * kGrBK / C::kK : nk_all;
   const int group = C::kSplit ? (int)blockIdx.x / S : (int)blockIdx.x;
   const int groups = C::kSplit ? (int)gridDim.x / S : (int)gridDim.x;
   volatile int* abort_flag = &s_abort;
@@ -357,8 +359,8 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
         int k0, k1;
         k_range(t, k0, k1);
         const int nrb = (w.rows + C::kRowBox - 1) / C::kRowBox;
-        const uint32_t bytes = C::kABytes + (uint32_t)nrb * C::kRowBox * kGrBK * 2;
-        for (int k = k0 * kGrBK; k < k1 * kGrBK; k += kGrBK) {
+        const uint32_t bytes = C::kABytes + (uint32_t)nrb * C::kRowBox * C::kK * 2;
+        for (int k = k0 * C::kK; k < k1 * C::kK; k += C::kK) {
           if (!wait_or_abort(&empty[slot], ph ^ 1u, abort_flag, a.status)) {
             ok = false;
             break;
@@ -370,15 +372,20 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
           if (TRANS) {  // [columns of y, reduction]: 128 x 64 boxes, K-major
 #pragma unroll
             for (int m = 0; m < NM; ++m)
-              tma_load_3d(st + m * 128 * kGrBK * 2, &wmap, k, w.n0 + 128 * m, w.e, &full[slot]);
-          } else {      // [reduction, columns of y]: 64 x 64 boxes, MN-major
+#pragma unroll
+              for (int h = 0; h < C::kK / kGrBK; ++h)
+                tma_load_3d(st + (m + h) * 128 * kGrBK * 2, &wmap, k + h * kGrBK, w.n0 + 128 * m, w.e,
+                            &full[slot]);
+          } else {      // [reduction, columns of y]: kK x 64 boxes, MN-major
 #pragma unroll
             for (int b = 0; b < 2 * NM; ++b)
-              tma_load_3d(st + b * 64 * kGrBK * 2, &wmap, w.n0 + 64 * b, k, w.e, &full[slot]);
+              tma_load_3d(st + b * 64 * C::kK * 2, &wmap, w.n0 + 64 * b, k, w.e, &full[slot]);
           }
-          for (int r = 0; r < nrb; ++r)
-            tma_load_2d(st + C::kABytes + r * (C::kRowBox * kGrBK * 2), &xmap, k,
-                        w.row0 + r * C::kRowBox, &full[slot]);
+#pragma unroll
+          for (int h = 0; h < C::kK / kGrBK; ++h)
+            for (int r = 0; r < nrb; ++r)
+              tma_load_2d(st + C::kABytes + h * C::kBHalf + r * (C::kRowBox * kGrBK * 2), &xmap,
+                          k + h * kGrBK, w.row0 + r * C::kRowBox, &full[slot]);
           ++issued;
           if (++slot == kStages) {
             slot = 0;
@@ -397,9 +404,8 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
       const uint32_t ring_s = smem_u32(ring);
       // descriptors of slot 0; a slot / K-step offset only moves the 14-bit start address
       const uint64_t adesc0 = TRANS ? smem_desc_sw128(ring_s, 16, 1024)
-                                    : smem_desc_sw128(ring_s, 64 * kGrBK * 2, 1024);
+                                    : smem_desc_sw128(ring_s, 64 * C::kK * 2, 1024);
       const uint64_t bdesc0 = smem_desc_sw128(ring_s + C::kABytes, 16, 1024);
-      constexpr int kAStep = TRANS ? 32 : 16 * 128;    // bytes per 16 reduction elements
       int slot = 0, unit = 0;
       uint32_t ph = 0, issued = 0;
       bool ok = true;
@@ -428,9 +434,12 @@ __global__ void __launch_bounds__(ColsCfg<ROWS, NM>::kThreads, 1)
             tc_fence_after();
             const uint64_t soff = (uint64_t)((slot * C::kStageBytes) >> 4);
 #pragma unroll
-            for (int k16 = 0; k16 < kGrBK / 16; ++k16) {
-              const uint64_t ak = adesc0 + soff + ((k16 * kAStep) >> 4);
-              const uint64_t bk = bdesc0 + soff + ((k16 * 32) >> 4);
+            for (int k16 = 0; k16 < C::kK / 16; ++k16) {
+              // K-major: 64 elements a box, 32 bytes a step; MN-major: 16 rows of 128 bytes a step
+              const int kmaj = (k16 % 4) * 32;
+              const uint64_t ak =
+                  adesc0 + soff + ((TRANS ? k16 / 4 * 128 * kGrBK * 2 + kmaj : k16 * 2048) >> 4);
+              const uint64_t bk = bdesc0 + soff + ((k16 / 4 * C::kBHalf + kmaj) >> 4);
 #pragma unroll
               for (int m = 0; m < NM; ++m)
                 tc_mma_bf16(d + m * ROWS, ak + ((m * 128 * kGrBK * 2) >> 4), bk, idesc, acc | k16);

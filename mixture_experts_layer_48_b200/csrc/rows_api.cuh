@@ -209,8 +209,9 @@ moe_status run_grouped(moe_ctx* c, const GroupedArgs& a, const void* W, const vo
                        : p.kind == GroupedPlan::kColsWide ? ColsCfg<kColsRows, 2>::kRowBox
                                                           : ColsCfg<kColsSmallRows, 1>::kRowBox;
   CUtensorMap wmap, xmap;
-  // transposed: boxes of 128 weight rows (columns of the result) x 64; else 64 x 64
-  if (!encode_planes(&wmap, W, c->E, K, N, TRANS ? 128 : kGrBK) ||
+  // weight boxes 64 columns wide; transposed: 128 rows (columns of the result), else a stage's
+  const int wrows = TRANS ? 128 : p.kind == GroupedPlan::kColsSmall ? ColsCfg<kColsSmallRows, 1>::kK : kGrBK;
+  if (!encode_planes(&wmap, W, c->E, K, N, wrows) ||
       !encode_rows(&xmap, x, a.R, a.Kred, box))
     return MOE_ERR_CUDA;
   return launch(c, -1, st, [&] {
