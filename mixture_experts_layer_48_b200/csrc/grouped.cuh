@@ -7,9 +7,9 @@
 //   transposed         y[r, :] = x[r, :] W[e]^T        x [R, N] -> y [R, K]       (gradient of x)
 //   weight gradient    dW[e]   = sum_r x[r, :]^T dy[r, :]   over e's rows         [E, K, N]
 //
-// Three kernel shapes, all persistent and warp-specialised (TMA producer warp, MMA issuer warp,
-// four or eight epilogue warps) around a ring of 128-byte-swizzled shared-memory stages of 64 reduction
-// elements:
+// Three kernel shapes, persistent and warp-specialised (TMA producer warp, MMA issuer warp, four or
+// eight epilogue warps) around a ring of 128-byte-swizzled shared-memory stages of 64 reduction
+// elements (128 where a tile has few rows):
 //
 //   grouped_cols_kernel   few rows per expert, bound by reading each touched expert's weights
 //                         once from HBM: 128 weight columns are the M operand, the rows N, and a
@@ -24,7 +24,7 @@
 // Measured (graph replay, one B200; copy bandwidth 6.46 TB/s, bf16 1.63 PFLOP/s in a burst and
 // 1.38 sustained):
 //   grouped_cols_kernel   64 rows over 32 experts, 2880 x 5760: 144 us, 6.5 TB/s; one token on 128
-//                         experts, 2880 x 2880, fp32: 20.1 us, 3.3 TB/s (about 5 us of it start-up)
+//                         experts, 2880 x 2880, fp32: 18.7 us, 3.6 TB/s (about 5 us of it start-up)
 //   grouped_rows_kernel   131,072 skewed rows, 2880 x 5760: 3.4 ms, 1.27 PFLOP/s; tensor pipe 85 %
 //                         busy, the rest is hand-over and the experts' padded last chunks
 //   grouped_wgrad_kernel  32,768 rows, 2880 x 5760: 1.0 ms, 1.06 PFLOP/s; tensor pipe 62 % busy
@@ -51,7 +51,7 @@
 namespace moe {
 
 constexpr int kGrMaxE = 256;
-constexpr int kGrBK = 64;           // reduction elements per stage (one 128-byte swizzle row)
+constexpr int kGrBK = 64;           // reduction elements of one 128-byte swizzle row (a stage, mostly)
 constexpr int kGrPieceStages = 10;  // stages per accumulator of an fp32 result (640 elements)
 
 MOE_DEVINL void tma_load_3d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
@@ -233,7 +233,9 @@ MOE_DEVINL void store4(void* out, size_t idx, float4 v) {
 template <int ROWS, int NM>
 struct ColsCfg {
   static constexpr bool kSplit = NM == 1;
-  static constexpr int kK = kSplit ? 2 * kGrBK : kGrBK;     // reduction elements per stage
+  // Reduction elements per stage: a 128-column tile takes 128 (32 KB of weights; with 64 it streamed
+  // 47 GB/s per SM instead of 64: one token down 20.0 against 18.7 us).
+  static constexpr int kK = kSplit ? 2 * kGrBK : kGrBK;
   static constexpr int kABytes = NM * 128 * kK * 2;
   static constexpr int kBHalf = ROWS * kGrBK * 2;           // 64 elements of every row
   static constexpr int kBBytes = ROWS * kK * 2;
