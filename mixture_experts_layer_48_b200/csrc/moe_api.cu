@@ -521,7 +521,7 @@ moe_status launch_route(moe_ctx* c, int T, const uint16_t* x, const uint16_t* Wr
     // tensor cores, then one block finishes the routing
     float* partial = reinterpret_cast<float*>(ws + rt.partial);
     MOE_TRY(launch(c, kKindRouter, st, [&] {
-      if (T <= kRouterSmallT) {  // small enough to run beside the previous call's down kernel
+      if (T <= kRouterSmallT) {  // small enough to be placed beside the previous call's down kernel
         if (nt8 <= 1) return launch_router_small<1>(st, x, Wr, T, H, E, zero4, n_zero4, rt, partial);
         if (nt8 <= 2) return launch_router_small<2>(st, x, Wr, T, H, E, zero4, n_zero4, rt, partial);
         if (nt8 <= 4) return launch_router_small<4>(st, x, Wr, T, H, E, zero4, n_zero4, rt, partial);

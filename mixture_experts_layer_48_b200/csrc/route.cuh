@@ -520,12 +520,15 @@ __global__ void __launch_bounds__(128)
   const int nk = min(H / kRouterHSlice - kc0, kc_per_split);
   const bool vec_w = (E % 8) == 0;
 
-  // x and W_router are the caller's inputs, which no kernel of this library writes: the loads
-  // and the products run before the dependency wait, everything this kernel writes after it
+  // x may be what the kernel in front of this one writes (moe_block_norm), so the loads follow the
+  // dependency wait; W_router's slice is only asked into L2 before it, which reads nothing yet
+  if (blockIdx.x == 0) prefetch_l2(Wr + (size_t)kc0 * kRouterHSlice * E, nk * kRouterHSlice * E);
   for (int i = tid; i < EP; i += blockDim.x) cnt[i] = 0;
   for (int i = tid; i < C::kStages * kRouterHSlice * WP; i += blockDim.x)
     wsm[i] = 0;  // padding experts stay zero
   __syncthreads();
+  pdl_wait();
+  pdl_launch_next();
 
   auto load_chunk = [&](int kc, int buf) {
     const int h0 = (kc0 + kc) * kRouterHSlice;
@@ -595,8 +598,6 @@ __global__ void __launch_bounds__(128)
     }
   }
   cp_async_wait<0>();
-  pdl_wait();
-  pdl_launch_next();
   zero_fill_f4(zero4, n_zero4);
   // C fragment: c0,c1 -> token 16w + lane/4, experts 8n + 2(lane%4) + {0,1}; c2,c3 -> token + 8
   if (partial != nullptr) {  // one slice of the hidden dimension: partial logits, no bias
@@ -626,10 +627,11 @@ __global__ void __launch_bounds__(128)
 // per block) in little shared memory: one 16-token tile that all four warps share, the experts
 // split over the warps (n-tile n on warp n % 4), and pipeline stages of one 16-deep K step (four
 // stages, at most 12 KB, up to 64 experts; two, 10 KB, at 128; 18 KB at 256).  Up to 128
-// experts a block fits on an SM beside a CTA of the streaming or expert-tile kernels, so its
-// loads and products run while the previous call's down kernel still holds the SMs, instead of
-// after it.  Every (token, expert) sum takes the same MMAs, on the same operands and in the same
-// K order, as in router_topk_kernel, so the partial logits are the same numbers.
+// experts a block fits on an SM beside a CTA of the streaming or expert-tile kernels, so it is
+// placed, and its W_router slice on the way to L2, while the previous call's down kernel still
+// holds the SMs.  (Eight or sixteen stages: 1 us less routing at 128 experts, none in the layer,
+// and up to 8 us more at 32.)  Every (token, expert) sum takes the same MMAs, on the same operands
+// and in the same K order, as in router_topk_kernel, so the partial logits are the same numbers.
 constexpr int kRouterSmallT = 16;
 constexpr int kRouterSmallXPitch = 24;  // elements; 48-byte rows keep ldmatrix conflict-free
 template <int NT8>
@@ -660,10 +662,13 @@ __global__ void __launch_bounds__(128)
   const int h_first = kc0 * kRouterHSlice;
   const bool vec_w = (E % 8) == 0;
 
-  // x and W_router are the caller's inputs, which no kernel of this library writes: the loads
-  // and the products run before the dependency wait, everything this kernel writes after it
+  // x may be what the kernel in front of this one writes (moe_block_norm), so the loads follow the
+  // dependency wait; W_router's slice is only asked into L2 before it, which reads nothing yet
+  prefetch_l2(Wr + (size_t)h_first * E, 16 * nsteps * E);
   for (int i = tid; i < C::kStages * C::kWStage; i += blockDim.x) wsm[i] = 0;  // padding experts
   __syncthreads();
+  pdl_wait();
+  pdl_launch_next();
 
   auto load_step = [&](int s, int buf) {
     const int h0 = h_first + 16 * s;
@@ -722,8 +727,6 @@ __global__ void __launch_bounds__(128)
     }
   }
   cp_async_wait<0>();
-  pdl_wait();
-  pdl_launch_next();
   zero_fill_f4(zero4, n_zero4);
   // C fragment: c0,c1 -> token lane/4, experts 8n + 2(lane%4) + {0,1}; c2,c3 -> token + 8
 #pragma unroll
