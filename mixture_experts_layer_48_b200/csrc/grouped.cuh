@@ -36,11 +36,14 @@
 // are negative, decrease or pass R give empty segments and set the status word.  Rows outside
 // every segment are neither used nor written.
 //
-// Sums: the tensor cores add into fp32 accumulators with truncation, an error that grows by about
-// 1.1e-9 (relative to the result) per reduction element (measured: 3.0e-6 at 2880, 6.3e-6 at
-// 5760, 1.9e-5 at 16384).  fp32 results therefore come from pieces of 640 elements, added in the
-// epilogue's registers with round to nearest (2.7e-7 ... 7e-7 in all); bf16 results, whose
-// rounding is 2e-3, take one piece.
+// Sums: the tensor cores add into fp32 accumulators with truncation, an error that grows with the
+// reduction: by about 1.1e-9 of the result per element on values of random signs (measured: 3.0e-6
+// at 2880, 6.3e-6 at 5760, 1.9e-5 at 16384), by 7e-9 where all terms have one sign (2.9e-2 at 4
+// million).  fp32 results therefore come from pieces of 640 elements, added in the epilogue's
+// registers with round to nearest (2.7e-7 ... 7e-7 in all on random signs, 4.5e-6 on one).  bf16
+// results, whose rounding is 3.9e-3, take one piece per reduction of a product (at most 32768
+// elements, 2.3e-4), and pieces of 65536 rows in the weight gradient (4.6e-4), whose reductions have
+// no such bound.
 #pragma once
 
 #include "common.cuh"
@@ -53,6 +56,7 @@ namespace moe {
 constexpr int kGrMaxE = 256;
 constexpr int kGrBK = 64;           // reduction elements of one 128-byte swizzle row (a stage, mostly)
 constexpr int kGrPieceStages = 10;  // stages per accumulator of an fp32 result (640 elements)
+constexpr int kGrPieceRowsBf16 = 65536;   // rows per accumulator of a bf16 weight gradient
 
 MOE_DEVINL void tma_load_3d(void* smem_dst, const CUtensorMap* map, int c0, int c1, int c2,
                             uint64_t* bar) {
@@ -728,8 +732,9 @@ MOE_DEVINL bool pair_collect(uint32_t taddr, int pieces, int& unit, uint64_t* ac
 // `pieces` accumulators in turn.  taddr: this warp's lanes and first column in buffer 0.  unit: the
 // accumulators handed over so far.  rows_ok <= 0: nothing to write, the hand-over only.
 // pieces = 0 writes zeros.  acc_read: this CTA's acc_empty or drained.  Returns false when a wait
-// gave up.
-template <bool F32>
+// gave up.  PIECES: whether a bf16 result may have more than one accumulator, and is summed as an
+// fp32 one.
+template <bool F32, bool PIECES>
 MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* acc_full,
                               uint64_t* acc_read, uint32_t* stage, int lane, void* out,
                               size_t row0, int rows_ok, int col0, int ld, volatile int* abort_flag,
@@ -746,6 +751,19 @@ MOE_DEVINL bool pair_epilogue(uint32_t taddr, int pieces, int& unit, uint64_t* a
 #pragma unroll
       for (int i = 0; i < 32; ++i) w[i] = __float_as_uint(sum[c][i]);
       pair_store<true>(w, stage, lane, out, row0, rows_ok, col0 + 32 * c, ld);
+    }
+  } else if constexpr (PIECES) {
+    float sum[4][32];
+    if (!pair_collect(taddr, pieces, unit, acc_full, acc_read, mine, sum, abort_flag, status))
+      return false;
+    if (!mine) return true;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        w[i] = cvt_bf16x2(sum[2 * c + i / 16][2 * (i % 16)], sum[2 * c + i / 16][2 * (i % 16) + 1]);
+      pair_store<false>(w, stage, lane, out, row0, rows_ok, col0 + 64 * c, ld);
     }
   } else {
     const int buf = unit & 1;
@@ -969,9 +987,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     int unit = 0;
     for (int t = pair; t < tiles; t += npairs) {
       const Tile w = tile_at(t);
-      if (!pair_epilogue<F32>(taddr, pieces, unit, acc_full, acc_read, stage, lane, a.out,
-                              (size_t)w.row0 + r0, w.rows - r0, w.n0 + 128 * half, a.Ncols,
-                              abort_flag, a.status))
+      if (!pair_epilogue<F32, false>(taddr, pieces, unit, acc_full, acc_read, stage, lane, a.out,
+                                     (size_t)w.row0 + r0, w.rows - r0, w.n0 + 128 * half, a.Ncols,
+                                     abort_flag, a.status))
         break;
     }
   }
@@ -983,11 +1001,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   if (warp == 1) tmem_dealloc_2sm(tmem_base, 512);
 }
 
-// Accumulators of one weight-gradient tile whose expert has cnt rows.
+// Rows per accumulator of a weight-gradient tile (whole stages), and the accumulators that cnt rows
+// take.
 template <bool F32>
-MOE_DEVINL int wgrad_pieces(int cnt) {
-  return F32 ? (cnt + kGrPieceStages * kGrBK - 1) / (kGrPieceStages * kGrBK) : cnt > 0;
-}
+MOE_DEVINL constexpr int wgrad_piece() { return F32 ? kGrPieceStages * kGrBK : kGrPieceRowsBf16; }
+template <bool F32>
+MOE_DEVINL int wgrad_pieces(int cnt) { return (cnt + wgrad_piece<F32>() - 1) / wgrad_piece<F32>(); }
 
 // Weight gradient.  Tile: 256 x 256 of dW[e]; the reduction runs over e's rows, 64 per stage,
 // from x [R, M] and dy [R, Ncols] as they lie (both MN-major: 64 x 64 boxes).  A segment's last
@@ -1006,7 +1025,11 @@ MOE_DEVINL int wgrad_pieces(int cnt) {
 // 128 rows of the tile; CTA (pair p, half h) gets those of its 128 / pairs rows from the other
 // pairs' CTAs of half h through distributed shared memory (the rings, idle by then), adds them in
 // pair order and writes them.
-template <bool F32, bool SPLIT>
+//
+// PIECES: calls whose segments may be longer than one bf16 accumulator takes (the host knows R
+// only).  Both ways in one kernel spilled, and cost the calls without such segments 3 %; summing
+// always costs them 2 % (8192 tokens, 2880 x 2880: 489 us, 503-514, 497-501).
+template <bool F32, bool SPLIT, bool PIECES>
 __global__ void __launch_bounds__(kWgradThreads, 1)
     grouped_wgrad_kernel(const GroupedArgs a, const __grid_constant__ CUtensorMap xmap,
                          const __grid_constant__ CUtensorMap dymap, const int pairs) {
@@ -1151,7 +1174,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
         const int cnt = seg.cnt[t / per];
         const uint32_t idesc = t % NT == NT - 1 ? idesc_last : idesc_all;
         const Range rg = range_of(cnt);
-        const int piece = F32 ? kGrPieceStages * kGrBK : max(cnt, 1);
+        constexpr int piece = wgrad_piece<F32>();
         for (int p0 = rg.r0; ok && p0 < rg.r1; p0 += piece, ++unit) {
           const int p1 = min(rg.r1, p0 + piece);
           const int buf = unit & 1;
@@ -1260,8 +1283,9 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       const int e = t / per, l = t - e * per;
       const int m0 = l / NT * 256 + rank * kPairHalf + 32 * q, n0 = l % NT * 256 + 128 * half;
       const int cnt = seg.cnt[e];
-      if (!pair_epilogue<F32>(taddr, wgrad_pieces<F32>(cnt), unit, acc_full, acc_read, stage, lane, a.out,
-                              (size_t)e * a.M + m0, a.M - m0, n0, a.Ncols, abort_flag, a.status))
+      if (!pair_epilogue<F32, PIECES>(taddr, wgrad_pieces<F32>(cnt), unit, acc_full, acc_read, stage, lane,
+                                      a.out, (size_t)e * a.M + m0, a.M - m0, n0, a.Ncols, abort_flag,
+                                      a.status))
         break;
     }
   }

@@ -370,8 +370,10 @@ moe_status moe_grouped_wgrad(moe_t c, int R, int K, int N, const int32_t* offset
   const int pairs = plan_wgrad(c, R, K, N);
   const int tiles = c->E * ((K + 255) / 256) * ((N + 255) / 256);
   const int grid = pairs > 1 ? tiles * 2 * pairs : c->num_sms / 2 * 2;
-  auto kernel = pairs > 1 ? (f32 ? grouped_wgrad_kernel<true, true> : grouped_wgrad_kernel<false, true>)
-                          : (f32 ? grouped_wgrad_kernel<true, false> : grouped_wgrad_kernel<false, false>);
+  auto kernel = grouped_wgrad_kernel<true, false, true>;
+  if (pairs > 1) kernel = f32 ? grouped_wgrad_kernel<true, true, true> : grouped_wgrad_kernel<false, true, true>;
+  else if (!f32) kernel = R > kGrPieceRowsBf16 ? grouped_wgrad_kernel<false, false, true>
+                                               : grouped_wgrad_kernel<false, false, false>;
   return launch(c, -1, st, [&] {
     if (!ready(c, kernel, kPairSmem)) return cudaErrorInvalidConfiguration;
     return launch_pdl_cluster(kernel, dim3(grid), dim3(kWgradThreads), (size_t)kPairSmem, 2 * pairs,
