@@ -17,6 +17,7 @@
 
 #include "common.cuh"
 #include "grouped.cuh"
+#include "ring.h"
 
 namespace moe {
 
@@ -130,6 +131,15 @@ MOE_DEVINL void ring_copy(uint8_t* to, const void* g, size_t row0, int rows, int
     bulk_g2s(to, static_cast<const uint8_t*>(g) + row0 * row_bytes, rows * row_bytes, bar);
 }
 
+// Thread 0, after a wait that gave up at row `lost` of a block's rows t, t + step, ... < T: waits for the
+// copies that are still on their way, so that none lands in shared memory that another block has by
+// then.
+MOE_DEVINL void ring_drain(uint64_t* full, int stages, int t, int step, int T, int lost) {
+  const int issued = ring_issued((lost - t) / step, stages, (T - t + step - 1) / step);
+  for (int j = ring_oldest(issued, stages); j < issued; ++j)
+    mbar_wait_bounded(&full[ring_slot(j, stages)], ring_parity(j, stages), kWaitLimitNs);
+}
+
 // r' = r + scale * gate * norm(y);  x = norm(r').  RT, YT: float or uint16_t (bf16).  One row a
 // block (or kRows) from global memory; STAGED: persistent blocks that work as the backward kernel's.
 template <int TPR, int VPT, typename RT, typename YT, bool STAGED>
@@ -181,7 +191,7 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads,
 
   int slot = 0, turn = 0;
   uint32_t phase = 0;
-  bool gave_up = false;
+  int lost = -1;          // first row whose copy this thread did not see arrive
   int t0 = blockIdx.x * C::kRows;
   do {
     const int t = t0 + sub;
@@ -191,9 +201,9 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads,
     const RT* resid = static_cast<const RT*>(a.resid) + base;
     const YT* yrow = static_cast<const YT*>(a.y) + base;
     if (STAGED) {
-      if (!gave_up && !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs)) {
+      if (lost < 0 && !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs)) {
         atomicOr(a.status, kStatusTimeout);
-        gave_up = true;
+        lost = t0;
       }
       const uint8_t* stage = ring + slot * a.stage_bytes;
       const int at = sub * a.H + 4 * lane;
@@ -204,7 +214,7 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads,
     auto refill = [&]() {   // after a barrier that follows the loads
       if (refilled) return;
       refilled = true;
-      if (threadIdx.x == 0 && !gave_up && t0 + (long long)a.stages * step < a.T)
+      if (threadIdx.x == 0 && lost < 0 && t0 + (long long)a.stages * step < a.T)
         fetch(t0 + a.stages * step, slot);
       if (++slot == a.stages) {
         slot = 0;
@@ -256,8 +266,8 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads,
     }
     t0 += step;
   } while (STAGED && t0 < a.T);
-  if (STAGED && gave_up && threadIdx.x == 0)   // what is still on its way must land first
-    for (int s = 0; s < a.stages; ++s) mbar_wait_bounded(&full[s], s < slot ? phase ^ 1u : phase, kWaitLimitNs);
+  if (STAGED && lost >= 0 && threadIdx.x == 0)
+    ring_drain(full, a.stages, blockIdx.x * C::kRows, step, a.T, lost);
 }
 
 // Backward.  With rh = r' * rstd_next and t = dx * w_next:
@@ -327,7 +337,8 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads, norm_backward_bloc
   // every thread of the block takes every step (the row sums are block-wide)
   int slot = 0, turn = 0;
   uint32_t phase = 0;
-  bool gave_up = false;   // a copy did not arrive: the status word says so, the rest is not waited for
+  int lost = -1;   // first row whose copy this thread did not see arrive: the status word says so, the
+                   // rest is not waited for
   for (int t0 = blockIdx.x * C::kRows; t0 < a.T; t0 += step) {
     const int t = t0 + sub;
     const bool live = C::kRows == 1 || t < a.T;
@@ -339,9 +350,9 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads, norm_backward_bloc
     const uint16_t* dxrow = a.dx + base;
     const YT* yrow = static_cast<const YT*>(a.y) + base;
     if (STAGED) {
-      if (!gave_up && !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs)) {
+      if (lost < 0 && !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs)) {
         atomicOr(a.status, kStatusTimeout);
-        gave_up = true;
+        lost = t0;
       }
       const uint8_t* stage = ring + slot * a.stage_bytes;
       const int at = sub * a.H + 4 * lane;
@@ -353,7 +364,7 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads, norm_backward_bloc
     // A barrier after the loads: the stage may be refilled.  The first row sum of a step is one.
     auto refill = [&]() {
       if (STAGED) {
-        if (threadIdx.x == 0 && !gave_up && t0 + (long long)a.stages * step < a.T)
+        if (threadIdx.x == 0 && lost < 0 && t0 + (long long)a.stages * step < a.T)
           fetch(t0 + a.stages * step, slot);
         if (++slot == a.stages) {
           slot = 0;
@@ -424,8 +435,8 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads, norm_backward_bloc
         }
     }
   }
-  if (STAGED && gave_up && threadIdx.x == 0)   // what is still on its way must land first
-    for (int s = 0; s < a.stages; ++s) mbar_wait_bounded(&full[s], s < slot ? phase ^ 1u : phase, kWaitLimitNs);
+  if (STAGED && lost >= 0 && threadIdx.x == 0)
+    ring_drain(full, a.stages, blockIdx.x * C::kRows, step, a.T, lost);
   const size_t row = (size_t)(blockIdx.x * C::kRows + sub) * a.H;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
