@@ -427,6 +427,13 @@ MOE_API moe_status moe_block_norm_backward(moe_t ctx, int T, moe_dtype resid_typ
  * is touched apart from the status word. */
 MOE_API moe_status moe_selftest_timeout(moe_t ctx, int limit_us, moe_stream_t stream);
 
+/* Self-test of the norms' timeout path: in the handle's following moe_block_norm and
+ * moe_block_norm_backward calls, the kernels that copy rows ahead (H up to 8192; forward, resid and y
+ * of at most 6 bytes an element together) take the copies of rows from_row and on as not arrived in
+ * time: they report it (MOE_ERR_TIMEOUT from moe_sync_status), leave results unset, wait for what is
+ * still on its way and return.  from_row < 0 ends it. */
+MOE_API moe_status moe_selftest_norm_timeout(moe_t ctx, int from_row);
+
 #ifdef __cplusplus
 }
 #endif

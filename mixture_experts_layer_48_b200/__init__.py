@@ -81,6 +81,7 @@ _SIGS = {
     "moe_block_norm_backward": (_c_int, [_vp, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp,
                                          _vp, _vp, _vp, _vp, _c_float, _vp, _vp, _vp, _vp, _vp, _vp,
                                          _vp, _sz, _vp]),
+    "moe_selftest_norm_timeout": (_c_int, [_vp, _c_int]),
     "moe_route_static": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
 }
 for _name, (_res, _args) in _SIGS.items():
@@ -540,3 +541,6 @@ class Moe:
 
     def selftest_timeout(self, limit_us: int, stream=None) -> None:
         _check(moe_selftest_timeout(self._h, limit_us, _stream(stream)), "moe_selftest_timeout")
+
+    def selftest_norm_timeout(self, from_row: int) -> None:
+        _check(moe_selftest_norm_timeout(self._h, from_row), "moe_selftest_norm_timeout")

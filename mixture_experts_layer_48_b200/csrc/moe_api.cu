@@ -93,6 +93,7 @@ struct moe_ctx {
   cudaEvent_t ev_fork = nullptr, ev_join = nullptr;
   // clusters of 2, 4 and 8 one-CTA-per-SM blocks that run at the same time (grouped products)
   int max_clusters[3] = {0, 0, 0};
+  int norm_lose_row = INT_MAX;   // moe_selftest_norm_timeout
   // kernels of rows_api.cuh whose shared-memory limit is set on this device
   static constexpr int kMaxReady = 64;
   const void* ready[kMaxReady];

@@ -98,6 +98,7 @@ struct NormArgs {
   int dy_f32;
   float *part_y, *part_x;                   // [row groups, H] partial column sums, or null
   int stages, stage_bytes;                  // the ring of the staged kernels
+  int lose_row;                             // rows from here on count as not arrived (self-test)
   uint32_t* status;
 };
 
@@ -201,7 +202,8 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads,
     const RT* resid = static_cast<const RT*>(a.resid) + base;
     const YT* yrow = static_cast<const YT*>(a.y) + base;
     if (STAGED) {
-      if (lost < 0 && !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs)) {
+      if (lost < 0 &&
+          (t0 >= a.lose_row || !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs))) {
         atomicOr(a.status, kStatusTimeout);
         lost = t0;
       }
@@ -350,7 +352,8 @@ __global__ void __launch_bounds__(RowCfg<TPR, VPT>::kThreads, norm_backward_bloc
     const uint16_t* dxrow = a.dx + base;
     const YT* yrow = static_cast<const YT*>(a.y) + base;
     if (STAGED) {
-      if (lost < 0 && !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs)) {
+      if (lost < 0 &&
+          (t0 >= a.lose_row || !mbar_wait_bounded(&full[slot], phase, kWaitLimitNs))) {
         atomicOr(a.status, kStatusTimeout);
         lost = t0;
       }

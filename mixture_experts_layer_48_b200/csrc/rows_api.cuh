@@ -285,6 +285,17 @@ RowPlan plan_rows(int stage_bytes, int max_blocks) {
   return best;
 }
 
+// What every norm kernel gets from the handle.
+NormArgs norm_args(const moe_ctx* c, int T, float scale) {
+  NormArgs a{};
+  a.T = T;
+  a.H = c->H;
+  a.scale = scale;
+  a.lose_row = c->norm_lose_row;
+  a.status = c->d_status;
+  return a;
+}
+
 // Persistent blocks of a call.
 template <int TPR, int VPT>
 int row_grid(const moe_ctx* c, int T, int blocks) {
@@ -436,11 +447,8 @@ moe_status moe_block_norm(moe_t c, int T, moe_dtype resid_type, moe_dtype y_type
       !all_aligned16({resid, y, w_post, gate, w_next, resid_out, x_bf16}) || !on_device(c))
     return MOE_ERR_ARG;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  NormArgs a{};
-  a.T = T;
-  a.H = c->H;
+  NormArgs a = norm_args(c, T, scale);
   a.eps = eps;
-  a.scale = scale;
   a.resid = resid;
   a.y = y;
   a.w_post = w_post;
@@ -474,6 +482,12 @@ moe_status moe_block_norm(moe_t c, int T, moe_dtype resid_type, moe_dtype y_type
       });
     });
   });
+}
+
+moe_status moe_selftest_norm_timeout(moe_t c, int from_row) {
+  if (!c) return MOE_ERR_ARG;
+  c->norm_lose_row = from_row < 0 ? INT_MAX : from_row;
+  return MOE_OK;
 }
 
 size_t moe_block_norm_workspace_bytes(moe_t c, int T) {
@@ -515,10 +529,7 @@ moe_status moe_block_norm_backward(moe_t c, int T, moe_dtype resid_type, moe_dty
                                 : nullptr;
   int parts = 0;   // partial rows that this call writes
   if (T > 0) {
-    NormArgs a{};
-    a.T = T;
-    a.H = c->H;
-    a.scale = scale;
+    NormArgs a = norm_args(c, T, scale);
     a.resid = resid;
     a.y = post || gated ? y : nullptr;
     a.w_post = w_post;
@@ -533,7 +544,6 @@ moe_status moe_block_norm_backward(moe_t c, int T, moe_dtype resid_type, moe_dty
     a.dy_f32 = dy_type == MOE_F32;
     a.part_x = part_x;
     a.part_y = part_y;
-    a.status = c->d_status;
     MOE_TRY(by_row_length(c->H / 4, [&](auto tpr, auto vpt) {
       constexpr int TPR = decltype(tpr)::value, VPT = decltype(vpt)::value;
       using C = RowCfg<TPR, VPT>;
