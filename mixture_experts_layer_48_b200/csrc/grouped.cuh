@@ -100,6 +100,27 @@ MOE_DEVINL bool wait_or_abort_cluster(uint64_t* bar, uint32_t parity, volatile i
     }
   }
 }
+// For a thread whose event may lie any time ahead, as the work before it is not its own: the limit
+// starts anew whenever *progress changes.
+MOE_DEVINL bool wait_or_abort_while(uint64_t* bar, uint32_t parity, const volatile uint32_t* progress,
+                                    volatile int* abort_flag, uint32_t* status) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = globaltimer_ns();
+  uint32_t seen = *progress;
+  while (true) {
+    if (*abort_flag) return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t now = *progress;
+    if (now != seen) {
+      seen = now;
+      t0 = globaltimer_ns();
+    } else if (globaltimer_ns() - t0 > kWaitLimitNs) {
+      atomicOr(status, kStatusTimeout);
+      *abort_flag = 1;
+      return false;
+    }
+  }
+}
 // The same answer for every lane, so that a warp leaves its loop as one (the tensor-memory loads
 // and barriers that follow are collective).
 MOE_DEVINL bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
@@ -1018,7 +1039,9 @@ MOE_DEVINL int wgrad_pieces(int cnt) { return (cnt + wgrad_piece<F32>() - 1) / w
 // waits for both.  No thread that writes memory arrives across the cluster, and ordinary stages take no
 // arrival from the odd CTA: the release waits for the thread's writes (0.45 us a stage from the
 // producer lane, half the kernel's rate; 0.5 us a tile from the masking warp).
-// Experts without rows get zeros.
+// Experts without rows get zeros.  The masking and reporting warps skip tiles without a ragged end, so
+// they may wait for their next one through most of a call, and a call can outlast the limit of a wait
+// (1.6 million rows of 32768 x 32768): their limit counts from the producer's last copies.
 //
 // SPLIT: where the tiles are too few for the GPU, a cluster of `pairs` (2 or 4) CTA pairs takes one
 // tile, each pair a run of the segment's stages.  Afterwards every CTA holds partial sums of its
@@ -1037,6 +1060,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
   __shared__ Segments seg;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
+  __shared__ uint32_t s_progress;   // changes as the producer goes round the ring
   uint8_t* ring = align1k(smem_raw);
   uint64_t* full = reinterpret_cast<uint64_t*>(ring + kPairStages * kPairStageBytes);
   uint64_t* empty = full + kPairStages;
@@ -1071,6 +1095,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
     }
     mbar_init(drain, 1);
     s_abort = 0;
+    s_progress = 0;
     fence_barrier_init();
     tma_prefetch_desc(&xmap);
     tma_prefetch_desc(&dymap);
@@ -1090,6 +1115,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
   const int pair = SPLIT ? (int)blockIdx.x / (2 * pairs) : (int)blockIdx.x >> 1;
   const int npairs = SPLIT ? tiles : (int)gridDim.x >> 1;
   volatile int* abort_flag = &s_abort;
+  volatile uint32_t* progress = &s_progress;
   // This pair's rows [r0, r1) of an expert's cnt.
   struct Range { int r0, r1; };
   auto range_of = [&](int cnt) {
@@ -1145,6 +1171,7 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
           if (++slot == kPairStages) {
             slot = 0;
             ph ^= 1u;
+            *progress = issued;
           }
         }
       }
@@ -1245,7 +1272,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
       const int slot = (it - 1) % kPairStages;
       const uint32_t ph = (ragged_ph >> slot) & 1u;
       ragged_ph ^= 1u << slot;
-      if (!warp_wait(&ragged[slot], ph, abort_flag, a.status)) break;
+      if (!__all_sync(0xffffffffu, wait_or_abort_while(&ragged[slot], ph, progress, abort_flag, a.status)))
+        break;
       // a row of a 64 x 64 box is 128 contiguous bytes (the swizzle permutes inside them)
       uint8_t* st = ring + slot * kPairStageBytes;
       const int pad = (16 - rem % 16) % 16;
@@ -1267,7 +1295,8 @@ __global__ void __launch_bounds__(kWgradThreads, 1)
         it += (rg.r1 - rg.r0 + kGrBK - 1) / kGrBK;
         if (rg.r1 == rg.r0 || rg.r1 % kGrBK == 0) continue;
         const int slot = (it - 1) % kPairStages;
-        if (!wait_or_abort(&masked[slot], (masked_ph >> slot) & 1u, abort_flag, a.status)) break;
+        if (!wait_or_abort_while(&masked[slot], (masked_ph >> slot) & 1u, progress, abort_flag, a.status))
+          break;
         masked_ph ^= 1u << slot;
         mbar_arrive_cluster(mapa_shared(smem_u32(&peer_masked[slot]), even));
       }
