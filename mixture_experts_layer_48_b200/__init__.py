@@ -147,7 +147,7 @@ class Moe:
         h = _vp()
         _check(moe_create(E, H, I, k, ctypes.byref(h)), "moe_create")
         self._h = h
-        self._ws = None
+        self._ws = self._ws_key = None
         self._device_index = torch.cuda.current_device()
 
     # -- lifetime --------------------------------------------------------------------
@@ -195,9 +195,19 @@ class Moe:
     def route_workspace_bytes(self, T: int) -> int:
         return moe_route_workspace_bytes(self._h, T)
 
-    def _workspace(self, nbytes: int, device) -> torch.Tensor:
-        if self._ws is None or self._ws.numel() < nbytes or self._ws.device != device:
+    def _workspace(self, nbytes: int, device, stream) -> torch.Tensor:
+        """A call's workspace, of the stream that it runs on.  The last call's serves again on the same
+        stream if it is large enough; a call that is being captured takes one of its graph's, which no
+        later call is given."""
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self._workspace(nbytes, device, None)
+        alone = device.type != "cuda" or torch.cuda.is_current_stream_capturing()
+        key = None if alone else (device, _raw_stream(device.index))
+        if alone or self._ws is None or self._ws_key != key or self._ws.numel() < nbytes:
+            self._ws = None     # back to its stream or graph before the next one is taken
             self._ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+            self._ws_key = key
         return self._ws
 
     # -- the layer -------------------------------------------------------------------
@@ -213,7 +223,7 @@ class Moe:
             inv_perm=torch.empty((T, k), dtype=torch.int32, device=dev),
         )
         need = self.route_workspace_bytes(T)
-        ws = self._workspace(need, dev) if workspace is None else workspace
+        ws = self._workspace(need, dev, stream) if workspace is None else workspace
         st = moe_route(self._h, T, _ptr(x, torch.bfloat16, "x", (T, H)),
                        _ptr(W_router, torch.bfloat16, "W_router", (H, E)),
                        _ptr(b_router, torch.float32, "b_router", (E,)),
@@ -230,7 +240,7 @@ class Moe:
         if out is None:
             out = torch.empty((T, H), dtype=torch.float32, device=x.device)
         need = self.workspace_bytes(T)
-        ws = self._workspace(need, x.device) if workspace is None else workspace
+        ws = self._workspace(need, x.device, stream) if workspace is None else workspace
         st = moe_forward(self._h, T, _ptr(x, torch.bfloat16, "x", (T, H)),
                          _ptr(W_router, torch.bfloat16, "W_router", (H, E)),
                          _ptr(b_router, torch.float32, "b_router", (E,)),
@@ -269,7 +279,7 @@ class Moe:
         need = moe_experts_workspace_bytes(self._h, R, S)
         if need == 0:
             raise ValueError("moe_experts: unsupported R or S")
-        ws = self._workspace(need, x_rows.device) if workspace is None else workspace
+        ws = self._workspace(need, x_rows.device, stream) if workspace is None else workspace
         st = moe_experts(self._h, R, S, _ptr(seg_counts, torch.int32, "seg_counts", (S, self.E)),
                          _ptr(x_rows, torch.bfloat16, "x_rows", (R, self.H)),
                          _ptr(row_w, torch.float32, "row_w", (R,)),
@@ -488,7 +498,7 @@ class Moe:
         if out is None:
             out = torch.empty((T, H), dtype=torch.float32, device=x.device)
         need = self.workspace_bytes_mxfp4(T)
-        ws = self._workspace(need, x.device) if workspace is None else workspace
+        ws = self._workspace(need, x.device, stream) if workspace is None else workspace
         st = moe_forward_mxfp4(self._h, T, _ptr(x, torch.bfloat16, "x", (T, H)),
                                _ptr(W_router, torch.bfloat16, "W_router", (H, E)),
                                _ptr(b_router, torch.float32, "b_router", (E,)),
@@ -505,7 +515,7 @@ class Moe:
         T = x.shape[0]
         out = torch.empty((T, self.H), dtype=torch.float32, device=x.device)
         need = moe_tune_workspace_bytes(self._h, T)
-        ws = self._workspace(need, x.device)
+        ws = self._workspace(need, x.device, stream)
         c = _c_int()
         st = moe_tune(self._h, T, _ptr(x, torch.bfloat16, "x"), _ptr(W_router, torch.bfloat16, "W_router"),
                       _ptr(b_router, torch.float32, "b_router"), _ptr(W_gate_up, torch.bfloat16, "W_gate_up"),
