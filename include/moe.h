@@ -360,7 +360,7 @@ typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
  * MOE_ERR_ARG; their segments count as empty.
  * moe_grouped_matmul: transpose = 0:  out[r, :] = x_rows[r, :] W[e]      x [R, K], out [R, N]
  *                     transpose = 1:  out[r, :] = x_rows[r, :] W[e]^T    x [R, N], out [R, K]
- *   out is bf16 (one rounding, to nearest even) or fp32.  R = 0 is a no-op.
+ *   out is bf16 (one rounding, to nearest even) or fp32.  R = 0 is a no-op (nor are offsets looked at).
  * moe_grouped_wgrad:  dW[e] [K, N] = sum over e's rows of x_rows[r, :]^T dy_rows[r, :], bf16 or
  *   fp32, written whole: experts without rows get zeros (R = 0: all of it).
  * Infinities and NaN in a row, or in an expert's weights, reach the results of that row or expert
@@ -387,7 +387,8 @@ MOE_API moe_status moe_swiglu_backward(moe_t ctx, int R, const void* dh_bf16, co
 
 /* The norms around a block (this layer, or any other whose output is [T, H]; H the handle's), in
  * one pass: the norm after the block, its gate and scale, the residual, and the norm before the
- * next block.  rms(v) = sqrt(mean(v^2) + eps), eps > 0.
+ * next block.  rms(v) = sqrt(mean(v^2) + eps), eps > 0; the squares are summed in fp32, so a row whose
+ * sum of squares passes 3.4e38 has an infinite rms.
  *   n          = y / rms(y) * w_post                  (w_post NULL: n = y)
  *   resid_out  = resid + scale * gate * n             (gate NULL: 1), rounded to resid's type
  *   x          = resid_out / rms(resid_out) * w_next  (w_next NULL: no x)

@@ -10,7 +10,9 @@ the compiled library -- there is no CPU fallback.
     r = layer.route(x, W_router, b_router)   # topk_idx, topk_w, expert_offsets, perm, inv_perm
 
 The pieces of a training step (grouped_matmul, grouped_wgrad, swiglu, swiglu_backward) and the
-norms around the block (block_norm, block_norm_backward, block) are methods of the same class.
+norms around the block (block_norm, block_norm_backward, block) are methods of the same class.  No
+method records anything for autograd: arguments may require a gradient, results never do, and the
+backward methods are called by name (from a torch.autograd.Function, for instance).
 """
 from __future__ import annotations
 

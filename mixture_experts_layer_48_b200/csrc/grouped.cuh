@@ -21,15 +21,18 @@
 //   grouped_wgrad_kernel  256 x 256 tiles of dW[e] per CTA pair, the expert's rows are the
 //                         reduction; both operands are MN-major
 //
-// Measured (graph replay, one B200; copy bandwidth 6.46 TB/s, bf16 1.63 PFLOP/s in a burst and
-// 1.38 sustained):
+// Measured (one B200; copy bandwidth 6.46 TB/s, bf16 1.63 PFLOP/s in a burst and 1.38 sustained).  The
+// two long ones as a burst of 12 calls, and after 3 s of calls, when the power cap holds the clock at
+// 1.1 to 1.5 GHz:
 //   grouped_cols_kernel   64 rows over 32 experts, 2880 x 5760: 144 us, 6.5 TB/s; one token on 128
 //                         experts, 2880 x 2880, fp32: 18.7 us, 3.6 TB/s (about 5 us of it start-up)
-//   grouped_rows_kernel   131,072 skewed rows, 2880 x 5760: 3.4 ms, 1.27 PFLOP/s; tensor pipe 85 %
-//                         busy, the rest is hand-over and the experts' padded last chunks
-//   grouped_wgrad_kernel  32,768 rows, 2880 x 5760: 1.0 ms, 1.06 PFLOP/s; tensor pipe 62 % busy
-//                         (16 stages a tile, each with a ragged end); 512 rows over 128 experts,
-//                         2880 x 2880: 462 us, 4.6 TB/s of writes
+//   grouped_rows_kernel   131,072 skewed rows, 2880 x 5760: 3.0 ms, 1.43 PFLOP/s, and 3.5 ms, 1.23;
+//                         tensor pipe 85 to 88 % busy, the rest is hand-over and the experts' padded last
+//                         chunks.  fp32 results cost 5 to 15 % more (32,768 rows, 2880 x 2880: 489 us for
+//                         440)
+//   grouped_wgrad_kernel  32,768 rows, 2880 x 5760: 0.97 ms, 1.12 PFLOP/s, and 1.12 ms, 0.97; tensor pipe
+//                         65 % busy (16 stages a tile, each with a ragged end); fp32 1.15 to 1.22 ms; 512
+//                         rows over 128 experts, 2880 x 2880: 462 to 700 us, 3.0 to 4.6 TB/s of writes
 //
 // The segments are read on the device: every CTA checks the E + 1 offsets and scans them in
 // shared memory, so there is no work-list kernel, no workspace and no host sync.  Offsets that

@@ -11,8 +11,8 @@
 //
 // Measured (graph replay, one B200, copy bandwidth 6.46 TB/s; rows of 2880): SwiGLU of 32,768 rows
 // 86 us forward, 138 us backward (6.6 and 6.8 TB/s); norms of 8189 rows, bf16 residual and fp32
-// block output, 42 us forward (5.6 TB/s: issue slots and row sums), of 32,768 fp32 rows 279 us
-// backward (6.75 TB/s).
+// block output, 42 us forward (5.6 TB/s: issue slots and row sums), of 32,768 rows backward 281 us with
+// an fp32 residual (6.7 TB/s) and 237 us with a bf16 one (5.6 TB/s).
 #pragma once
 
 #include "common.cuh"
@@ -114,7 +114,9 @@ MOE_DEVINL float4 post_factor(const NormArgs& a, int v) {
 // threads (64 registers) with three vectors a thread, 1280 (51) with fewer; backward 512 (128), 768
 // (85) and 1024 (64).  A backward row on 512 threads with two vectors takes two blocks of 64
 // registers, some of them spilled (16,000 rows of 4096: 199 us, 217 with one block).  More vectors:
-// one block.
+// one block.  Rows of over 6144 spill there, backward, up to 744 bytes a thread with eight vectors: fp32
+// residual and block output, 2^26 elements, 4.8 TB/s at rows of 8192 (282 us), 3.1 at 16384 (439 us);
+// forward 5.4 and 4.8.
 template <int TPR, int VPT>
 constexpr int norm_forward_blocks() {
   return VPT > 3 ? 1 : (VPT == 3 ? 1024 : 1280) / RowCfg<TPR, VPT>::kThreads;

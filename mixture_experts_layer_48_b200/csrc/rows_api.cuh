@@ -133,6 +133,8 @@ double grouped_us(long long tiles, int slots, double stages, double stage_us, do
 
 // The constants are fitted to 176 measured calls (1..128 experts of 2..640 rows, four weight
 // shapes; bf16, graph replay): the choice costs 0.4 % over the best kernel of each, 12 % at worst.
+// It sees the mean rows of an expert only; on skewed calls (32 experts, 64..2048 tokens of 4 choices,
+// popularity falling as rank^-0.5 .. rank^-1.5) it costs up to 4 %, mostly under 0.5 %.
 // Some of them, us as 128-column tiles / split in two / in four / 256-column tiles / pairs:
 //   1 expert of 4 rows, 2880 x 2880          18.0 / 11.7 / 8.8 / 22.7 / 19.0
 //   8 experts of 4 rows, 2880 x 2880         36.7 / 30.5 / 31.1 / 25.6 / 35.6

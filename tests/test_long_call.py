@@ -38,3 +38,25 @@ def test_the_last_segment_of_a_long_call():
             _near(dW[e][c, -64:], ref, hi - lo, f"expert {e}")
     del x, dW
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("transpose", [False, True], ids=["product", "transposed"])
+def test_products_of_the_most_rows(transpose):
+    """2^28 rows, the first and last outside of the segments: offsets near the end of 32 bits' reach."""
+    R, n = 1 << 28, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.empty((R, n), dtype=torch.bfloat16, device="cuda").uniform_(0.5, 1.0, generator=g)
+    W = torch.empty((3, n, n), dtype=torch.bfloat16, device="cuda").uniform_(0.5, 1.0, generator=g)
+    bounds = [1, R // 2 + 77, R // 2 + 77, R - 1]
+    o = torch.tensor(bounds, dtype=torch.int32, device="cuda")
+    out = torch.full((R, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    layer = moe.Moe(3, 64, 64, 1)
+    layer.grouped_matmul(x, W, o, transpose=transpose, out=out)
+    assert layer.sync_status() == moe.MOE_OK
+    assert (out[0] == 7).all() and (out[-1] == 7).all()
+    for e in range(3):
+        w = W[e].double().t() if transpose else W[e].double()
+        for lo in range(bounds[e], bounds[e + 1], 1 << 24):
+            hi = min(lo + (1 << 24), bounds[e + 1])
+            _near(out[lo:hi], x[lo:hi].double() @ w, n, f"expert {e}, rows from {lo}")
