@@ -281,16 +281,9 @@ MOE_DEVINL uint8_t* align1k(uint8_t* p) {
 // ---- programmatic dependent launch ------------------------------------------------------------
 // Every kernel of the layer first waits for the kernel before it on the stream (a no-op when it
 // was launched without the programmatic-serialisation attribute), then lets the next kernel
-// launch.  Work placed before pdl_wait() may only touch memory no earlier kernel still uses, and no
-// tensor of the caller is that: any of them may be the result of the call in front.
+// launch.  Work placed before pdl_wait() may only touch memory no earlier kernel still uses.
 MOE_DEVINL void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 MOE_DEVINL void pdl_launch_next() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-// Asks for n bf16 values at p to be brought into L2, by all threads of the block.  Reads nothing
-// that a thread sees, so it may come before pdl_wait().
-MOE_DEVINL void prefetch_l2(const uint16_t* p, int n) {
-  for (int i = threadIdx.x * 64; i < n; i += blockDim.x * 64)
-    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
-}
 
 // ---- misc ----------------------------------------------------------------------------
 MOE_DEVINL void named_bar_sync(int id, int nthreads) {

@@ -465,6 +465,14 @@ __global__ void __launch_bounds__(1024)
   for (int i = tid; i < o.n_zero; i += blockDim.x) o.zero_i32[i] = 0;
 }
 
+// Asks for n bf16 values at p to be brought into L2, by all threads of the block.  Reads nothing
+// that a thread sees, so it may come before pdl_wait(), where no load of a caller's tensor may: any of
+// them can be the result of the call in front.
+MOE_DEVINL void prefetch_l2(const uint16_t* p, int n) {
+  for (int i = threadIdx.x * 64; i < n; i += blockDim.x * 64)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
+}
+
 // ---------------------------------------------------------------------------------------
 // Large T, step 1: logits of 64 tokens x all experts on the tensor cores, then top-k, softmax
 // and the block's expert histogram.  grid ceil(T/64), block 128 (4 warps x 16 tokens).
