@@ -346,9 +346,9 @@ MOE_API moe_status moe_route_static(moe_t ctx, int T, const void* x_bf16,
  * they may be parts of larger arrays.  Buffers that a call writes overlap none of its others unless
  * it says so.
  * Every sum is fp32.  The tensor cores truncate when they add, so long products are added up from
- * pieces: relative to the sum of its terms' magnitudes an fp32 result is off by at most 5e-6 and
- * 2^-25 for every 640 terms, a bf16 one by 2^-10 before its rounding.  Results of one build on one
- * device do not change from call to call. */
+ * pieces: relative to the sum of its terms' magnitudes an fp32 result is off by at most 1e-5 and
+ * 2^-24 for every 640 terms, a bf16 one before its rounding by 2^-10 and 2^-24 for every 65536.
+ * Results of one build on one device do not change from call to call. */
 typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
 
 /* Products grouped by expert.  The handle's E experts; W [E, K, N] bf16, K and N multiples of 8 up

@@ -119,6 +119,13 @@ def _ptr(t: torch.Tensor | None, dtype: torch.dtype, name: str, shape=None) -> i
     return t.data_ptr()
 
 
+def _scratch(ws: torch.Tensor, device) -> torch.Tensor:
+    """A caller's workspace, which the kernels take for numel() bytes on the device of their tensors."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}, got one on {ws.device}")
+    return ws
+
+
 # The current stream's handle; torch's own short way to it where it has one (a tenth of a
 # microsecond instead of three for a Stream object).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
@@ -225,7 +232,7 @@ class Moe:
             inv_perm=torch.empty((T, k), dtype=torch.int32, device=dev),
         )
         need = self.route_workspace_bytes(T)
-        ws = self._workspace(need, dev, stream) if workspace is None else workspace
+        ws = self._workspace(need, dev, stream) if workspace is None else _scratch(workspace, dev)
         st = moe_route(self._h, T, _ptr(x, torch.bfloat16, "x", (T, H)),
                        _ptr(W_router, torch.bfloat16, "W_router", (H, E)),
                        _ptr(b_router, torch.float32, "b_router", (E,)),
@@ -242,7 +249,7 @@ class Moe:
         if out is None:
             out = torch.empty((T, H), dtype=torch.float32, device=x.device)
         need = self.workspace_bytes(T)
-        ws = self._workspace(need, x.device, stream) if workspace is None else workspace
+        ws = self._workspace(need, x.device, stream) if workspace is None else _scratch(workspace, x.device)
         st = moe_forward(self._h, T, _ptr(x, torch.bfloat16, "x", (T, H)),
                          _ptr(W_router, torch.bfloat16, "W_router", (H, E)),
                          _ptr(b_router, torch.float32, "b_router", (E,)),
@@ -281,7 +288,7 @@ class Moe:
         need = moe_experts_workspace_bytes(self._h, R, S)
         if need == 0:
             raise ValueError("moe_experts: unsupported R or S")
-        ws = self._workspace(need, x_rows.device, stream) if workspace is None else workspace
+        ws = self._workspace(need, x_rows.device, stream) if workspace is None else _scratch(workspace, x_rows.device)
         st = moe_experts(self._h, R, S, _ptr(seg_counts, torch.int32, "seg_counts", (S, self.E)),
                          _ptr(x_rows, torch.bfloat16, "x_rows", (R, self.H)),
                          _ptr(row_w, torch.float32, "row_w", (R,)),
@@ -465,8 +472,8 @@ class Moe:
         ws = workspace
         if ws is None and not (w_post is None and gate is None and w_next is None):
             ws = like.new_empty((self.block_norm_workspace_bytes(T),), dtype=torch.uint8)
-        elif ws is not None and ws.get_device() != self._device_index:
-            raise ValueError(f"workspace must be on cuda:{self._device_index}, got {ws.device}")
+        elif ws is not None:
+            _scratch(ws, like.device)
         ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
         st = moe_block_norm_backward(
             self._h, T, *types, *args, scale, pn, ptr(out["dresid"]), ptr(out["dy"]),
@@ -500,7 +507,7 @@ class Moe:
         if out is None:
             out = torch.empty((T, H), dtype=torch.float32, device=x.device)
         need = self.workspace_bytes_mxfp4(T)
-        ws = self._workspace(need, x.device, stream) if workspace is None else workspace
+        ws = self._workspace(need, x.device, stream) if workspace is None else _scratch(workspace, x.device)
         st = moe_forward_mxfp4(self._h, T, _ptr(x, torch.bfloat16, "x", (T, H)),
                                _ptr(W_router, torch.bfloat16, "W_router", (H, E)),
                                _ptr(b_router, torch.float32, "b_router", (E,)),

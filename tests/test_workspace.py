@@ -92,3 +92,31 @@ def test_tensors_of_the_host_are_still_refused():
             call(d["x"].cpu(), *args)
         call(d["x"], *args)
     assert layer.sync_status() == moe.MOE_OK
+
+
+@pytest.mark.parametrize("name", ["forward", "block", "route"])
+def test_workspaces_that_are_not_plain_device_memory_are_refused(name):
+    layer, d, args = _layer(8, 5)
+    call = _calls(layer, args, torch.ones(H, device="cuda"))[name]
+    n = max(layer.workspace_bytes(8), layer.route_workspace_bytes(8))
+    call(d["x"], workspace=torch.empty((n,), dtype=torch.uint8, device="cuda"))
+    for bad in (torch.empty((n,), dtype=torch.uint8), torch.empty((1,), dtype=torch.uint8, device="cuda").expand(n),
+                torch.empty((n, 2), dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError):
+            call(d["x"], workspace=bad)
+    with pytest.raises(moe.MoeError):
+        call(d["x"], workspace=torch.empty((16,), dtype=torch.uint8, device="cuda"))
+    assert layer.sync_status() == moe.MOE_OK
+
+
+def test_workspaces_of_the_norms_backward_pass_that_are_not_plain_device_memory_are_refused():
+    layer = moe.Moe(1, H, 64, 1)
+    r, w = torch.randn((4, H), device="cuda"), torch.ones((H,), device="cuda")
+    f = layer.block_norm(r, w_next=w)
+    call = lambda ws: layer.block_norm_backward(r, f["x"], r, rstd_next=f["rstd_next"], w_next=w, workspace=ws)  # noqa: E731
+    n = layer.block_norm_workspace_bytes(4)
+    call(torch.empty((n,), dtype=torch.uint8, device="cuda"))
+    for bad in (torch.empty((n,), dtype=torch.uint8), torch.empty((1,), dtype=torch.uint8, device="cuda").expand(n)):
+        with pytest.raises(ValueError):
+            call(bad)
+    assert layer.sync_status() == moe.MOE_OK
